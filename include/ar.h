@@ -390,6 +390,100 @@ ar_status ar_linear(const uint16_t* X, int64_t n, int64_t in, const uint16_t* Wq
  * of a LLaMA-style down projection).  a, b, y: count bf16 bits. */
 ar_status ar_silu_mul(const uint16_t* a, const uint16_t* b, int64_t count, uint16_t* y, void* stream);
 
+/* ---------------------------------------------------------------------------
+ * 8-bit chain: the layer chain above with e4m3 operands ("[SGLang] AutoRound ...":
+ * quantised checkpoints are served through quantised products; the pages give no
+ * arithmetic for them, the formulas below are this library's).
+ *
+ * A scaled tensor is a pair (q, scale): q in e4m3 (4 exponent, 3 mantissa bits, at
+ * most 448, no infinity), and one fp32 scale per block of 128 columns -- of one row
+ * (activations, scale [rows, ceil(cols/128)]) or of 128 rows (weights, scale
+ * [ceil(rows/128), ceil(cols/128)]); the last blocks may be partial.  It stands for
+ * scale * q.  Of a block with values x:
+ *     scale = max |x| / 448      (1 if that is 0)
+ *     q     = e4m3(x / scale)    (nearest, ties to even; the quotient is rounded
+ *                                 once to fp32 before)
+ * The maximum ignores NaN: a NaN stays in its place.  A block that holds an infinity
+ * gets an infinite scale and reads back as NaN.
+ *
+ * Pitches (ld...) are in elements and at least the row's length; scales and offsets
+ * are contiguous.  Calls run on the current device, which owns `stream` and every
+ * pointer.  None needs a workspace, so calls on different streams may overlap; all
+ * may be captured into a graph.  Same inputs give bit-identical outputs.
+ * ------------------------------------------------------------------------- */
+
+/* Root-mean-square norm with the residual's addition:
+ *     h = x + residual                                (fp32; x alone if NULL)
+ *     v = h * (1 / sqrt(mean(h^2) + eps)) * weight    (fp32, over each row)
+ *   x        [rows, cols] fp32 or bf16 (x_dtype), pitch ldx.
+ *   residual [rows, cols] fp32 or bf16 (r_dtype), pitch ldr, or NULL.
+ *   weight   [cols] fp32 or bf16 (w_dtype), or NULL (ones).
+ *   sum      [rows, cols] r_dtype out, pitch lds: h, rounded once; may be NULL, and may be
+ *            `residual` itself.  (The norm reads the unrounded h.)
+ *   y        [rows, cols] bf16 out, pitch ldy: v, rounded once; may be NULL.
+ *   q, scale v as a scaled tensor with row blocks, q pitch ldq; may be NULL.
+ * Outputs must not overlap the inputs otherwise.  cols at most 32768 (else
+ * AR_EUNSUPPORTED).  rows == 0 or cols == 0: no-op.
+ * AR_EINVAL: eps negative or not finite, sum without residual, q without scale, no
+ * output at all, a NULL x, a pitch below cols, a misaligned pointer (its element). */
+ar_status ar_rms_norm(const void* x, ar_dtype x_dtype, int64_t ldx, int64_t rows, int64_t cols,
+                      const void* residual, ar_dtype r_dtype, int64_t ldr, const void* weight,
+                      ar_dtype w_dtype, float eps, void* sum, int64_t lds, uint16_t* y, int64_t ldy,
+                      uint8_t* q, int64_t ldq, float* scale, void* stream);
+
+/* Quantise to scaled tensors: `count` matrices [rows, cols], fp32 or bf16 (x_dtype), pitch
+ * ldx, rows * ldx elements apart; q likewise with ldq.  block_rows 1: scale [count, rows,
+ * ceil(cols/128)]; 128: scale [count, ceil(rows/128), ceil(cols/128)].
+ * AR_EINVAL: block_rows not 1 or 128, NULL pointers, a pitch below cols.  Nothing to do
+ * (a size of 0): no-op. */
+ar_status ar_quant_scaled(const void* x, ar_dtype x_dtype, int64_t ldx, int64_t count, int64_t rows,
+                          int64_t cols, int32_t block_rows, uint8_t* q, int64_t ldq, float* scale,
+                          void* stream);
+
+/* silu(a) * b in fp32 (as ar_silu_mul, without its rounding to bf16) as a scaled tensor
+ * with row blocks.  a, b: [rows, cols] bf16, pitches lda, ldb (two halves of one
+ * gate-and-up output, for example). */
+ar_status ar_silu_mul_scaled(const uint16_t* a, int64_t lda, const uint16_t* b, int64_t ldb, int64_t rows,
+                             int64_t cols, uint8_t* q, int64_t ldq, float* scale, void* stream);
+
+/* Y = bf16(X W^T + add) of scaled tensors, on the tensor cores:
+ *     Y[n, o] = sum_b x_scale[n, b] * w_scale[o/128, b] * sum_{k in block b} X[n, k] * W[o, k]
+ * each block's products summed by the tensor cores in fp32, the blocks added in fp32 in
+ * order within a share of K and the shares in order, one rounding to bf16.
+ *   X [n, in], W [out, in]: e4m3, 16-byte aligned, `in` and the pitches multiples of 16.
+ *   add [n, out] bf16 or NULL, added in fp32;  Y [n, out] bf16 out (must not overlap add
+ *   unless it is add itself with the same pitch).
+ *   status: as for ar_linear.
+ * AR_EINVAL: NULL or misaligned pointers, bad sizes or pitches.  AR_EUNSUPPORTED: n or
+ * out above 2^30.  n == 0: no-op. */
+ar_status ar_linear_scaled(const uint8_t* X, int64_t ldx, const float* x_scale, int64_t n, int64_t in,
+                           const uint8_t* W, int64_t ldw, const float* w_scale, int64_t out,
+                           const uint16_t* add, int64_t ldadd, uint16_t* Y, int64_t ldy,
+                           int32_t* status, void* stream);
+
+/* Products grouped by expert: row r of X belongs to expert e where offsets[e] <= r <
+ * offsets[e+1], and Y[r] = bf16(X[r] (W_hi[e] + W_lo[e])^T).
+ *   X [n, in] bf16, 16-byte aligned;  W_hi, W_lo [experts, out, in] bf16, 16-byte aligned,
+ *   rows ldw apart, matrices out * ldw apart (W_lo may be NULL: see ar_dequant);  `in` and
+ *   the pitches ldx, ldw multiples of 8.
+ *   offsets [experts + 1] int32 on the device, not decreasing, within [0, n]; experts may be
+ *   empty.  Rows of Y before offsets[0] and from offsets[experts] on are left as they were.
+ *   Offsets that break this are clamped into [0, n]: no access leaves X or Y, but which
+ *   rows are written is then undefined.
+ *   Y [n, out] bf16 out.  status: as for ar_linear.
+ * AR_EINVAL as ar_linear_scaled; AR_EUNSUPPORTED: more than 1024 experts, n or
+ * experts * out above 2^30.  n == 0: no-op. */
+ar_status ar_grouped_linear(const uint16_t* X, int64_t ldx, int64_t n, int64_t in, const int32_t* offsets,
+                            int64_t experts, const uint16_t* W_hi, const uint16_t* W_lo, int64_t ldw,
+                            int64_t out, uint16_t* Y, int64_t ldy, int32_t* status, void* stream);
+
+/* The same of scaled tensors, with ar_linear_scaled's arithmetic: w_scale [experts,
+ * ceil(out/128), ceil(in/128)]; `in` and the pitches ldx, ldw multiples of 16. */
+ar_status ar_grouped_linear_scaled(const uint8_t* X, int64_t ldx, const float* x_scale, int64_t n,
+                                   int64_t in, const int32_t* offsets, int64_t experts, const uint8_t* W,
+                                   int64_t ldw, const float* w_scale, int64_t out, uint16_t* Y,
+                                   int64_t ldy, int32_t* status, void* stream);
+
 /* Size of the fixed device scratch array used by ar_tune_layer_static (64 MiB). */
 #define AR_STATIC_SCRATCH_BYTES (64ull << 20)
 

@@ -17,7 +17,7 @@ import sys
 PKG = os.path.dirname(os.path.abspath(__file__))
 ROOT = os.path.dirname(PKG)
 CSRC = os.path.join(PKG, "csrc")
-SOURCES = ["api.cu", "quant_kernels.cu", "gemm_sm100.cu"]
+SOURCES = ["api.cu", "quant_kernels.cu", "gemm_sm100.cu", "scaled_rows.cu", "scaled_product.cu", "scaled_api.cu"]
 LIB = os.path.join(PKG, "libar.so")
 
 NVCC_FLAGS = [

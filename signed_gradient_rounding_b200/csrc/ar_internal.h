@@ -293,4 +293,9 @@ cudaError_t launch_gemm(EpiKind kind, int bn, const GemmMaps& maps, const GemmAr
 cudaError_t make_tmap_bf16(CUtensorMap* map, const void* base, uint64_t rows, uint64_t cols,
                            uint32_t box_rows);
 
+// The same for rows of row_bytes bytes, pitch_bytes apart (a multiple of 16), box
+// [box_rows, 128 bytes]: operands of either element size by their bytes.
+cudaError_t make_tmap_bytes(CUtensorMap* map, const void* base, uint64_t rows, uint64_t row_bytes,
+                            uint64_t pitch_bytes, uint32_t box_rows);
+
 }  // namespace ar
