@@ -15,6 +15,8 @@
 //     swizzle, so both operand types share one pipeline.
 //   * skinny_kernel: few rows per expert, bound by the weight's bytes; each weight
 //     byte goes from HBM straight into the registers of the warp that multiplies it.
+#include <stdlib.h>
+
 #include <atomic>
 
 #include "ar_device.cuh"
@@ -41,25 +43,42 @@ __device__ __forceinline__ void expert_rows(const ProductArgs& a, int e, int& r0
 // Tile kernel
 // ---------------------------------------------------------------------------
 
-constexpr int kTileWarps = 10;  // producer, MMA issuer, 8 epilogue warps
+// Three warpgroups: producer, one or two MMA issuers and a scale loader; two of epilogue.
+constexpr int kTileWarps = 12;
+constexpr int kLoaderWarp = 3;
+constexpr int kEpiWarp0 = 4;
 constexpr int kTileThreads = 32 * kTileWarps;
 constexpr int kMaxStages = 8;
 constexpr int kRowTile = 128;     // rows per CTA: tensor-memory lanes
 constexpr int kRasterM = 8;       // row blocks that share a sweep over the weight's columns
 constexpr int kKBytes = 128;      // bytes of K per stage and row
 
+constexpr int kScaleKb = 4;     // K blocks per slot of the scale ring
+constexpr int kScaleSlots = 4;
+
 struct TileSmem {
   uint64_t full[kMaxStages], empty[kMaxStages];
-  uint64_t tfull[2], tempty[2];
-  uint64_t drain;
+  uint64_t tfull[4], tempty[4];  // accumulator b of column half h: 2 b + h (one half: b)
+  uint64_t sfull[kScaleSlots], sempty[kScaleSlots];
+  uint64_t drain[2];
   uint32_t tmem_base;
   int abort_flag;
+  // e4m3: scales of kScaleKb K blocks per slot, of the CTA's rows and column halves
+  float xs[kScaleSlots][kScaleKb][kRowTile];
+  float ws[kScaleSlots][kScaleKb][2];
+  uint4 out[8][128];         // per epilogue warp: 32 rows x 32 columns of Y
   int cum[kMaxExperts + 1];  // row blocks of the experts before e
 };
 
-template <bool kPair, int kBN>
+template <bool kF8, bool kPair, int kBN>
 struct TileCfg {
+  // e4m3 tiles of 256 columns are two column halves of 128, each with its own MMAs,
+  // accumulators and issuing warp: the hand-over of a half after every K block then
+  // overlaps the other half's MMAs.
+  static constexpr int kHalves = kF8 && kBN == 256 ? 2 : 1;
+  static constexpr int kMmaN = kBN / kHalves;
   static constexpr int kBRows = kPair ? kBN / 2 : kBN;  // weight rows this CTA stages
+  static constexpr int kWBoxes = kPair ? kHalves : 1;   // ... in so many loads (a pair's half: 64 rows in each CTA)
   static constexpr int kABytes = kRowTile * kKBytes;
   static constexpr int kStageBytes = kABytes + kBRows * kKBytes;
   static constexpr int kStages = kStageBytes <= 32768 ? 6 : 4;
@@ -142,36 +161,177 @@ __device__ __forceinline__ void store8(const ProductArgs& a, int64_t row, int co
   }
 }
 
-// acc += s * v, two columns at a time.
-__device__ __forceinline__ void fma2(uint64_t& acc, uint32_t v0, uint32_t v1, uint64_t s2) {
-  uint64_t v;
-  asm("mov.b64 %0, {%1, %2};" : "=l"(v) : "r"(v0), "r"(v1));
-  asm("fma.rn.f32x2 %0, %1, %2, %0;" : "+l"(acc) : "l"(v), "l"(s2));
+// Columns [col, col + 32) of a warp's 32 rows (row0 ..; those from r1 on belong to others),
+// lane = row, x the lane's values.  Through shared memory, so that a store instruction
+// writes 64 contiguous bytes of 8 rows: stored from where they are, 16 bytes of 32 rows at
+// a time, the columns of a 256 x 256 tile took 7500 cycles.  The buffer's 16-byte units are
+// swizzled by the row pair: no bank conflicts either way.
+__device__ __forceinline__ void store_cols32(const ProductArgs& a, uint4* buf, int row0, int r1, int col, int lane,
+                                             float (&x)[32]) {
+  if (row0 >= r1 || col >= a.out) return;  // the whole warp
+  if (!a.vec_y || col + 32 > a.out) {
+    if (row0 + lane < r1) {
+#pragma unroll
+      for (int c = 0; c < 4; ++c) store8(a, row0 + lane, col + c * 8, reinterpret_cast<float(&)[8]>(x[c * 8]));
+    }
+    return;
+  }
+  const int r = lane >> 2, unit = lane & 3;  // of the coalesced side: rows r + 8 i
+  const int own = lane * 4, own_swz = (lane >> 1) & 3;
+  if (a.add) {
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      const int rr = r + 8 * i;
+      if (row0 + rr < r1)
+        buf[rr * 4 + (unit ^ ((rr >> 1) & 3))] =
+            *reinterpret_cast<const uint4*>(a.add + static_cast<int64_t>(row0 + rr) * a.ldadd + col + unit * 8);
+    }
+    __syncwarp();
+#pragma unroll
+    for (int c = 0; c < 4; ++c) {
+      const uint4 v = buf[own + (c ^ own_swz)];
+      const uint32_t w[4] = {v.x, v.y, v.z, v.w};
+#pragma unroll
+      for (int j = 0; j < 4; ++j) {
+        x[c * 8 + 2 * j] += __uint_as_float(w[j] << 16);
+        x[c * 8 + 2 * j + 1] += __uint_as_float(w[j] & 0xFFFF0000u);
+      }
+    }
+    __syncwarp();
+  }
+#pragma unroll
+  for (int c = 0; c < 4; ++c)
+    buf[own + (c ^ own_swz)] = make_uint4(pack2(x[c * 8], x[c * 8 + 1]), pack2(x[c * 8 + 2], x[c * 8 + 3]),
+                                          pack2(x[c * 8 + 4], x[c * 8 + 5]), pack2(x[c * 8 + 6], x[c * 8 + 7]));
+  __syncwarp();
+#pragma unroll
+  for (int i = 0; i < 4; ++i) {
+    const int rr = r + 8 * i;
+    if (row0 + rr < r1)
+      *reinterpret_cast<uint4*>(a.Y + static_cast<int64_t>(row0 + rr) * a.ldy + col + unit * 8) =
+          buf[rr * 4 + (unit ^ ((rr >> 1) & 3))];
+  }
+  __syncwarp();
 }
 
-__device__ __forceinline__ void unpack2(uint64_t v, float& lo, float& hi) {
-  asm("mov.b64 {%0, %1}, %2;" : "=f"(lo), "=f"(hi) : "l"(v));
+// tcgen05 and TMA instructions issued by the whole warp with a predicate that holds in
+// one lane (elect_one).  In a branch of one lane the compiler can neither keep their
+// operands in uniform registers nor compute them there, which cost about 70 cycles per
+// instruction; a K block of the tile kernel has 8 of them.
+template <bool kF8, bool kPair>
+__device__ __forceinline__ void umma(uint32_t leader, uint32_t d_tmem, uint64_t a_desc, uint64_t b_desc, uint32_t idesc,
+                                     uint32_t accumulate) {
+#define AR_UMMA(GROUP, KIND)                                                                     \
+  asm volatile(                                                                                  \
+      "{\n\t.reg .pred p, q;\n\t"                                                                \
+      "setp.ne.b32 p, %4, 0;\n\t"                                                                \
+      "setp.ne.b32 q, %5, 0;\n\t"                                                                \
+      "@q tcgen05.mma.cta_group::" GROUP ".kind::" KIND " [%0], %1, %2, %3, p;\n\t}" ::"r"(d_tmem), \
+      "l"(a_desc), "l"(b_desc), "r"(idesc), "r"(accumulate), "r"(leader)                         \
+      : "memory")
+  if (kF8 && kPair)
+    AR_UMMA("2", "f8f6f4");
+  else if (kF8)
+    AR_UMMA("1", "f8f6f4");
+  else if (kPair)
+    AR_UMMA("2", "f16");
+  else
+    AR_UMMA("1", "f16");
+#undef AR_UMMA
 }
 
-// e4m3 operands, fp32 accumulation (format fields 0 = e4m3), issued by one thread.
-__device__ __forceinline__ void umma_f8(uint32_t d_tmem, uint64_t a_desc, uint64_t b_desc, uint32_t idesc,
-                                        uint32_t accumulate) {
+// Arrive on `bar` (pair: on the barrier at this offset in both CTAs) once the MMAs issued so far are done.
+template <bool kPair>
+__device__ __forceinline__ void umma_commit_if(uint32_t leader, uint32_t bar) {
+  if (kPair)
+    asm volatile(
+        "{\n\t.reg .pred q;\n\tsetp.ne.b32 q, %2, 0;\n\t"
+        "@q tcgen05.commit.cta_group::2.mbarrier::arrive::one.shared::cluster.multicast::cluster.b64 [%0], %1;\n\t}" ::"r"(
+            bar),
+        "h"((uint16_t)3), "r"(leader)
+        : "memory");
+  else
+    asm volatile(
+        "{\n\t.reg .pred q;\n\tsetp.ne.b32 q, %1, 0;\n\t"
+        "@q tcgen05.commit.cta_group::1.mbarrier::arrive::one.shared::cluster.b64 [%0];\n\t}" ::"r"(bar),
+        "r"(leader)
+        : "memory");
+}
+
+__device__ __forceinline__ void expect_tx_if(uint32_t leader, uint32_t bar, uint32_t bytes) {
   asm volatile(
-      "{\n\t.reg .pred p;\n\t"
-      "setp.ne.b32 p, %4, 0;\n\t"
-      "tcgen05.mma.cta_group::1.kind::f8f6f4 [%0], %1, %2, %3, p;\n\t}" ::"r"(d_tmem),
-      "l"(a_desc), "l"(b_desc), "r"(idesc), "r"(accumulate)
+      "{\n\t.reg .pred q;\n\tsetp.ne.b32 q, %2, 0;\n\t"
+      "@q mbarrier.arrive.expect_tx.shared::cta.b64 _, [%0], %1;\n\t}" ::"r"(bar),
+      "r"(bytes), "r"(leader)
       : "memory");
 }
 
-__device__ __forceinline__ void umma_f8_pair(uint32_t d_tmem, uint64_t a_desc, uint64_t b_desc, uint32_t idesc,
-                                             uint32_t accumulate) {
+template <bool kPair>
+__device__ __forceinline__ void tma_load_if(uint32_t leader, uint32_t dst, const CUtensorMap* map, int32_t x, int32_t y,
+                                            uint32_t bar) {
+  if (kPair)
+    asm volatile(
+        "{\n\t.reg .pred q;\n\tsetp.ne.b32 q, %5, 0;\n\t"
+        "@q cp.async.bulk.tensor.2d.cta_group::2.shared::cluster.global.tile.mbarrier::complete_tx::bytes"
+        " [%0], [%1, {%2, %3}], [%4];\n\t}" ::"r"(dst),
+        "l"(reinterpret_cast<uint64_t>(map)), "r"(x), "r"(y), "r"(bar), "r"(leader)
+        : "memory");
+  else
+    asm volatile(
+        "{\n\t.reg .pred q;\n\tsetp.ne.b32 q, %5, 0;\n\t"
+        "@q cp.async.bulk.tensor.2d.shared::cluster.global.tile.mbarrier::complete_tx::bytes"
+        " [%0], [%1, {%2, %3}], [%4];\n\t}" ::"r"(dst),
+        "l"(reinterpret_cast<uint64_t>(map)), "r"(x), "r"(y), "r"(bar), "r"(leader)
+        : "memory");
+}
+
+// Wait for the phase of `bar` with this parity (whole warps).  After timeout_ns, or once
+// another role has given up (*abort), it records kDevTimeout in *status, raises *abort and
+// returns false.  The test is one instruction of the warp, so its lanes leave together.
+__device__ __forceinline__ bool wait_bar(uint32_t bar, uint32_t parity, volatile int* abort, int* status,
+                                         uint64_t timeout_ns) {
+  uint32_t polls = 0;
+  uint64_t t0 = 0;
+  while (!mbar_try_wait(bar, parity)) {
+    if ((++polls & 255u) == 0) {
+      const uint64_t now = globaltimer_ns();
+      if (t0 == 0) t0 = now;
+      if (__any_sync(__activemask(), now - t0 > timeout_ns || *abort)) {
+        atomicCAS(status, kDevOk, kDevTimeout);
+        *abort = 1;
+        return false;
+      }
+    }
+  }
+  return true;
+}
+
+// A 4-byte asynchronous copy, and an arrive once the thread's copies so far are done.
+__device__ __forceinline__ void cp_async4(float* dst, const float* src) {
+  asm volatile("cp.async.ca.shared.global [%0], [%1], 4;" ::"r"(smem_u32(dst)), "l"(src) : "memory");
+}
+
+__device__ __forceinline__ void cp_async_arrive(uint64_t* bar) {
+  asm volatile("cp.async.mbarrier.arrive.noinc.shared::cta.b64 [%0];" ::"r"(smem_u32(bar)) : "memory");
+}
+
+// Arrive on the pair leader's barrier (a shared::cluster address).  No memory is handed
+// over with it: the accumulator's values are in registers (tcgen05.wait::ld) and
+// tcgen05.fence orders the loads, so the release stays at CTA scope; at cluster scope it
+// waits for every outstanding access of the thread, and the hand-off took four times as long.
+__device__ __forceinline__ void mbar_arrive_remote(uint32_t cluster_addr) {
+  asm volatile("mbarrier.arrive.shared::cluster.b64 _, [%0];" ::"r"(cluster_addr) : "memory");
+}
+
+// 1 in one lane of the (converged) warp, the same on every call.
+__device__ __forceinline__ uint32_t elect_one() {
+  uint32_t p;
   asm volatile(
       "{\n\t.reg .pred p;\n\t"
-      "setp.ne.b32 p, %4, 0;\n\t"
-      "tcgen05.mma.cta_group::2.kind::f8f6f4 [%0], %1, %2, %3, p;\n\t}" ::"r"(d_tmem),
-      "l"(a_desc), "l"(b_desc), "r"(idesc), "r"(accumulate)
-      : "memory");
+      "elect.sync _|p, 0xffffffff;\n\t"
+      "selp.u32 %0, 1, 0, p;\n\t}"
+      : "=r"(p));
+  return p;
 }
 
 __host__ __device__ constexpr uint32_t umma_idesc_f8(int M, int N) {
@@ -182,25 +342,30 @@ template <bool kF8, bool kPair, int kBN>
 __global__ void __launch_bounds__(kTileThreads, 1)
     tile_kernel(const __grid_constant__ CUtensorMap tmX, const __grid_constant__ CUtensorMap tmW,
                 const __grid_constant__ CUtensorMap tmWlo, const __grid_constant__ ProductArgs args) {
-  using C = TileCfg<kPair, kBN>;
+  using C = TileCfg<kF8, kPair, kBN>;
   extern __shared__ uint8_t smem_raw[];
   uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
   TileSmem* sm = reinterpret_cast<TileSmem*>(smem + C::kBarOffset);
   volatile int* abort_flag = &sm->abort_flag;
-  const int warp = threadIdx.x >> 5;
+  const int warp = __shfl_sync(0xffffffffu, static_cast<int>(threadIdx.x >> 5), 0);  // warp-uniform
   const int lane = threadIdx.x & 31;
   const uint32_t rank = kPair ? cluster_ctarank() : 0u;
 
   if (warp == 1 && lane == 0) {
     for (int s = 0; s < C::kStages; ++s) {
       mbar_init(&sm->full[s], 1);
-      mbar_init(&sm->empty[s], 1);
+      mbar_init(&sm->empty[s], C::kHalves);  // one commit per issuer
     }
-    for (int b = 0; b < 2; ++b) {
+    for (int b = 0; b < 2 * C::kHalves; ++b) {
       mbar_init(&sm->tfull[b], 1);
-      mbar_init(&sm->tempty[b], (kPair ? 2 : 1) * 8);  // one arrive per epilogue warp
+      mbar_init(&sm->tempty[b], (kPair ? 2 : 1) * 8 / C::kHalves);  // one arrive per epilogue warp that reads it
     }
-    mbar_init(&sm->drain, 1);
+    for (int b = 0; b < kScaleSlots; ++b) {
+      mbar_init(&sm->sfull[b], 32);  // every thread of the loader warp
+      mbar_init(&sm->sempty[b], 8);
+    }
+    mbar_init(&sm->drain[0], 1);
+    mbar_init(&sm->drain[1], 1);
     sm->abort_flag = 0;
     fence_mbar_init();
   }
@@ -256,39 +421,38 @@ __global__ void __launch_bounds__(kTileThreads, 1)
   const int64_t stride = kPair ? gridDim.x >> 1 : gridDim.x;
   const int nkb = args.nkb;
   const int k_total = (!kF8 && args.W_lo) ? 2 * nkb : nkb;
-  // e4m3: the accumulator is handed over after every K block; bf16: after the last.
-  const int k_chunk = kF8 ? 1 : k_total;
+  const uint32_t bar_full = smem_u32(sm->full), bar_empty = smem_u32(sm->empty);
+  const uint32_t bar_tfull = smem_u32(sm->tfull), bar_tempty = smem_u32(sm->tempty);
 
-  if (warp == 0) {
-    if (lane == 0) {
-      // ------------------------------------------------------------ producer
+  // Registers: the launch's 12 warps at 168 become 4 at 56 and 8 at 224.
+  if (warp < kEpiWarp0) {
+    asm volatile("setmaxnreg.dec.sync.aligned.u32 56;");
+    if (warp == 0) {
+      // -------------------------------------------------------------- producer
+      const uint32_t leader = elect_one();
+      const uint32_t leader_full = kPair ? mapa_shared(bar_full, 0) : 0u;  // completion counts on the pair leader's
       int stage = 0;
       uint32_t phase = 0, issued_mask = 0, issued_parity = 0;
       bool ok = true;
       for (int64_t t = unit0; ok && t < num_units; t += stride) {
         const Unit u = find_unit(args, sm->cum, t, num_n, C::kBM, kBN);
         const int x_row = u.m0 + static_cast<int>(rank) * kRowTile;
-        const int w_row = u.e * args.out + u.n0 + static_cast<int>(rank) * C::kBRows;
+        const int w_row = u.e * args.out + u.n0 + static_cast<int>(rank) * (C::kBRows / C::kWBoxes);
         for (int kb = 0; kb < k_total; ++kb) {
-          if (!mbar_wait<kPair>(&sm->empty[stage], phase ^ 1, abort_flag, args.status, args.timeout_ns)) {
+          if (!wait_bar(bar_empty + 8 * stage, phase ^ 1, abort_flag, args.status, args.timeout_ns)) {
             ok = false;
             break;
           }
-          uint8_t* sx = smem + stage * C::kStageBytes;
-          uint8_t* sw = sx + C::kABytes;
+          const uint32_t sx = smem_u32(smem) + stage * C::kStageBytes;
           const bool lo = !kF8 && kb >= nkb;
           const int k = (lo ? kb - nkb : kb) * kKBytes;  // bytes: the maps are byte maps
-          const CUtensorMap* mw = lo ? &tmWlo : &tmW;
-          if (kPair) {
-            if (rank == 0) mbar_arrive_expect_tx(&sm->full[stage], 2 * C::kStageBytes);
-            const uint32_t leader = mapa_shared(smem_u32(&sm->full[stage]), 0);
-            tma_load_2d_pair(sx, &tmX, k, x_row, leader);
-            tma_load_2d_pair(sw, mw, k, w_row, leader);
-          } else {
-            mbar_arrive_expect_tx(&sm->full[stage], C::kStageBytes);
-            tma_load_2d(sx, &tmX, k, x_row, &sm->full[stage]);
-            tma_load_2d(sw, mw, k, w_row, &sm->full[stage]);
-          }
+          if (!kPair || rank == 0) expect_tx_if(leader, bar_full + 8 * stage, (kPair ? 2 : 1) * C::kStageBytes);
+          const uint32_t bar = (kPair ? leader_full : bar_full) + 8 * stage;
+          tma_load_if<kPair>(leader, sx, &tmX, k, x_row, bar);
+#pragma unroll
+          for (int b = 0; b < C::kWBoxes; ++b)
+            tma_load_if<kPair>(leader, sx + C::kABytes + b * (C::kBRows / C::kWBoxes) * kKBytes, lo ? &tmWlo : &tmW, k,
+                               w_row + b * C::kMmaN, bar);
           issued_mask |= 1u << stage;
           issued_parity = (issued_parity & ~(1u << stage)) | (phase << stage);
           if (++stage == C::kStages) {
@@ -309,167 +473,180 @@ __global__ void __launch_bounds__(kTileThreads, 1)
             if (issued_mask & (1u << s)) mbar_wait_drain(&sm->full[s], (issued_parity >> s) & 1u, args.timeout_ns);
         }
       }
-    }
-  } else if (warp == 1) {
-    if (lane == 0 && rank == 0) {
-      // ------------------------------------------------------------ MMA issuer
-      constexpr int kM = kPair ? 2 * kRowTile : kRowTile;
-      constexpr uint32_t idesc = kF8 ? umma_idesc_f8(kM, kBN) : umma_idesc_bf16(kM, kBN);
-      int stage = 0, acc = 0;
-      uint32_t phase = 0, acc_phase = 0;
-      bool ok = true;
-      for (int64_t t = unit0; ok && t < num_units; t += stride) {
-        for (int kb0 = 0; ok && kb0 < k_total; kb0 += k_chunk) {
-          if (!mbar_wait<kPair>(&sm->tempty[acc], acc_phase ^ 1, abort_flag, args.status, args.timeout_ns)) {
-            ok = false;
-            break;
-          }
-          tc_fence_after();
-          const uint32_t d_tmem = tmem_base + acc * kBN;
-          for (int kb = kb0; kb < kb0 + k_chunk; ++kb) {
-            if (!mbar_wait<kPair>(&sm->full[stage], phase, abort_flag, args.status, args.timeout_ns)) {
-              ok = false;
-              break;
-            }
+    } else if (warp <= C::kHalves) {
+      if (rank == 0) {
+        // ------------------------------------------------------------ MMA issuers
+        constexpr int kM = kPair ? 2 * kRowTile : kRowTile;
+        constexpr uint32_t idesc = kF8 ? umma_idesc_f8(kM, C::kMmaN) : umma_idesc_bf16(kM, C::kMmaN);
+        const int half = warp - 1;
+        const uint32_t leader = elect_one();
+        const uint64_t desc0 = umma_desc_sw128(smem_u32(smem));
+        const uint32_t b_off = C::kABytes + half * (C::kBRows / C::kHalves) * kKBytes;
+        int stage = 0, acc = 0;
+        uint32_t phase = 0, acc_phase = 0;
+        bool ok = true;
+        for (int64_t t = unit0; ok && t < num_units; t += stride) {
+          for (int kb = 0; kb < k_total; ++kb) {
+            const uint32_t bar_acc = 8 * (acc * C::kHalves + half);
+            const bool first = kF8 || kb == 0, last = kF8 || kb == k_total - 1;
+            // both tests in flight at once: each takes over 100 cycles, passed or not
+            const bool free = !first || mbar_try_wait(bar_tempty + bar_acc, acc_phase ^ 1);
+            const bool here = mbar_try_wait(bar_full + 8 * stage, phase);
+            if (!free) ok = wait_bar(bar_tempty + bar_acc, acc_phase ^ 1, abort_flag, args.status, args.timeout_ns);
+            if (ok && !here) ok = wait_bar(bar_full + 8 * stage, phase, abort_flag, args.status, args.timeout_ns);
+            if (!ok) break;
             tc_fence_after();
-            const uint32_t addr = smem_u32(smem + stage * C::kStageBytes);
-            const uint64_t a_desc = umma_desc_sw128(addr), b_desc = umma_desc_sw128(addr + C::kABytes);
+            const uint32_t d_tmem = tmem_base + acc * kBN + half * C::kMmaN;
+            const uint64_t a_desc = desc0 + stage * (C::kStageBytes >> 4);
+            const uint64_t b_desc = a_desc + (b_off >> 4);
 #pragma unroll
-            for (int k = 0; k < 4; ++k) {  // 32 bytes of K each: 2 descriptor units
-              const uint32_t accum = ((kb - kb0) | k) != 0 ? 1u : 0u;
-              if (kF8 && kPair)
-                umma_f8_pair(d_tmem, a_desc + 2 * k, b_desc + 2 * k, idesc, accum);
-              else if (kF8)
-                umma_f8(d_tmem, a_desc + 2 * k, b_desc + 2 * k, idesc, accum);
-              else if (kPair)
-                umma_bf16_pair(d_tmem, a_desc + 2 * k, b_desc + 2 * k, idesc, accum);
-              else
-                umma_bf16(d_tmem, a_desc + 2 * k, b_desc + 2 * k, idesc, accum);
+            for (int k = 0; k < 4; ++k)  // 32 bytes of K each: 2 descriptor units
+              umma<kF8, kPair>(leader, d_tmem, a_desc + 2 * k, b_desc + 2 * k, idesc, !first || k > 0);
+            umma_commit_if<kPair>(leader, bar_empty + 8 * stage);
+            if (last) {
+              umma_commit_if<kPair>(leader, bar_tfull + bar_acc);
+              acc ^= 1;
+              if (acc == 0) acc_phase ^= 1;
             }
-            if (kPair)
-              umma_commit_pair_both(&sm->empty[stage]);
-            else
-              umma_commit(&sm->empty[stage]);
             if (++stage == C::kStages) {
               stage = 0;
               phase ^= 1;
             }
           }
-          if (!ok) break;
+        }
+        // Every MMA this warp's leader issued has completed once `drain` flips.
+        if (leader) {
           if (kPair)
-            umma_commit_pair_both(&sm->tfull[acc]);
+            umma_commit_pair_local(&sm->drain[half]);
           else
-            umma_commit(&sm->tfull[acc]);
-          acc ^= 1;
-          if (acc == 0) acc_phase ^= 1;
+            umma_commit(&sm->drain[half]);
+        }
+        __syncwarp();
+        mbar_wait_drain(&sm->drain[half], 0, args.timeout_ns);
+      }
+    } else if (kF8 && warp == kLoaderWarp) {
+      // ---------------------------------------------------------- scale loader
+      // Four rows per thread, kScaleKb blocks per slot, asynchronous copies: a row's
+      // scales are contiguous along K, so the copies of a warp touch one 32-byte
+      // sector per row, and run slots ahead of the epilogue.
+      int slot = 0;
+      uint32_t phase = 0;
+      bool ok = true;
+      for (int64_t t = unit0; ok && t < num_units; t += stride) {
+        const Unit u = find_unit(args, sm->cum, t, num_n, C::kBM, kBN);
+        const float* x[4];
+#pragma unroll
+        for (int r = 0; r < 4; ++r)
+          x[r] = args.xs +
+                 static_cast<int64_t>(min(u.m0 + static_cast<int>(rank) * kRowTile + lane + 32 * r, u.r1 - 1)) * nkb;
+        // threads 0 .. 7 also bring the weight's scales: block lane / 2 of half lane % 2
+        const int nb = min((u.n0 + (lane & 1) * (kBN / 2)) >> 7, args.out_blocks - 1);
+        const float* w = args.ws + (static_cast<int64_t>(u.e) * args.out_blocks + nb) * nkb;
+        for (int kb0 = 0; kb0 < nkb; kb0 += kScaleKb) {
+          if (!wait_bar(smem_u32(&sm->sempty[slot]), phase ^ 1, abort_flag, args.status, args.timeout_ns)) {
+            ok = false;
+            break;
+          }
+#pragma unroll
+          for (int i = 0; i < kScaleKb; ++i) {
+            const int kb = min(kb0 + i, nkb - 1);
+#pragma unroll
+            for (int r = 0; r < 4; ++r) cp_async4(&sm->xs[slot][i][lane + 32 * r], x[r] + kb);
+          }
+          if (lane < 2 * kScaleKb) cp_async4(&sm->ws[slot][lane >> 1][lane & 1], w + min(kb0 + (lane >> 1), nkb - 1));
+          cp_async_arrive(&sm->sfull[slot]);
+          if (++slot == kScaleSlots) {
+            slot = 0;
+            phase ^= 1;
+          }
         }
       }
-      // Every MMA this thread issued has completed once `drain` flips.
-      if (kPair)
-        umma_commit_pair_local(&sm->drain);
-      else
-        umma_commit(&sm->drain);
-      mbar_wait_drain(&sm->drain, 0, args.timeout_ns);
+      asm volatile("cp.async.wait_all;" ::: "memory");
     }
   } else {
+    asm volatile("setmaxnreg.inc.sync.aligned.u32 224;");
     // -------------------------------------------------------------- epilogue
     constexpr int kNC = kBN / 2;       // columns per thread
     const int quarter = warp & 3;      // tensor-memory lanes this warp may access
-    const int half = (warp - 2) >> 2;  // column half of the tile
+    const int half = (warp - kEpiWarp0) >> 2;  // column half of the tile
     const uint32_t t_lane = tmem_base + (static_cast<uint32_t>(quarter * 32) << 16) + half * kNC;
-    const uint32_t leader_tempty0 = kPair ? mapa_shared(smem_u32(&sm->tempty[0]), 0) : 0u;
-    const uint32_t leader_tempty1 = kPair ? mapa_shared(smem_u32(&sm->tempty[1]), 0) : 0u;
+    uint4* out_buf = sm->out[warp - kEpiWarp0];
+    // This warp's accumulator barriers (the empty one is the pair leader's): + 8 kHalves for the second buffer.
+    const uint32_t my_tfull = bar_tfull + (C::kHalves == 2 ? 8 * half : 0);
+    const uint32_t my_tempty =
+        (kPair ? mapa_shared(bar_tempty, 0) : bar_tempty) + (C::kHalves == 2 ? 8 * half : 0);
     auto release = [&](int buf) {
       tc_fence_before();
       __syncwarp();
-      if (lane == 0) {
-        if (kPair)
-          mbar_arrive_cluster(buf ? leader_tempty1 : leader_tempty0);
-        else
-          mbar_arrive(&sm->tempty[buf]);
-      }
+      if (lane == 0) mbar_arrive_remote(my_tempty + 8 * C::kHalves * buf);
     };
-    int acc_buf = 0;
-    uint32_t acc_phase = 0;
+    int acc_buf = 0, slot = 0;
+    uint32_t acc_phase = 0, slot_phase = 0;
     bool ok = true;
     for (int64_t t = unit0; ok && t < num_units; t += stride) {
       const Unit u = find_unit(args, sm->cum, t, num_n, C::kBM, kBN);
-      const int row = u.m0 + static_cast<int>(rank) * kRowTile + quarter * 32 + lane;
-      const bool row_ok = row < u.r1;
+      const int row0 = u.m0 + static_cast<int>(rank) * kRowTile + quarter * 32;  // the warp's 32 rows
       const int col0 = u.n0 + half * kNC;
       if constexpr (kF8) {
-        uint64_t acc[kNC / 2];
+        float acc[kNC];
 #pragma unroll
-        for (int i = 0; i < kNC / 2; ++i) acc[i] = 0ull;
-        // Row and weight scales of four K blocks at a time, loaded one group ahead.
-        const float* xs = args.xs + static_cast<int64_t>(row_ok ? row : u.r1 - 1) * nkb;
-        const float* ws =
-            args.ws + (static_cast<int64_t>(u.e) * args.out_blocks + min(col0 >> 7, args.out_blocks - 1)) * nkb;
-        float xn[4], wn[4];
-#pragma unroll
-        for (int i = 0; i < 4; ++i) {
-          xn[i] = __ldg(xs + min(i, nkb - 1));
-          wn[i] = __ldg(ws + min(i, nkb - 1));
-        }
-        for (int kb0 = 0; ok && kb0 < nkb; kb0 += 4) {
-          float s[4];
-#pragma unroll
-          for (int i = 0; i < 4; ++i) {
-            s[i] = __fmul_rn(xn[i], wn[i]);
-            xn[i] = __ldg(xs + min(kb0 + 4 + i, nkb - 1));
-            wn[i] = __ldg(ws + min(kb0 + 4 + i, nkb - 1));
-          }
-#pragma unroll
-          for (int i = 0; i < 4; ++i) {
-            if (kb0 + i >= nkb) break;
-            if (!mbar_wait<kPair>(&sm->tfull[acc_buf], acc_phase, abort_flag, args.status, args.timeout_ns, false)) {
+        for (int i = 0; i < kNC; ++i) acc[i] = 0.f;
+#pragma unroll 1
+        for (int kb = 0; kb < nkb; ++kb) {
+          const int i = kb % kScaleKb;
+          if (i == 0) {
+            if (!wait_bar(smem_u32(&sm->sfull[slot]), slot_phase, abort_flag, args.status, args.timeout_ns)) {
               ok = false;
               break;
             }
-            tc_fence_after();
-            uint64_t s2;
-            asm("mov.b64 %0, {%1, %1};" : "=l"(s2) : "f"(s[i]));
-#pragma unroll
-            for (int g = 0; g < kNC / 32; ++g) {
-              uint32_t r[32];
-              tmem_ld_32cols(t_lane + acc_buf * kBN + g * 32, r);
-              tmem_ld_wait();
-              if (g == kNC / 32 - 1) release(acc_buf);
-#pragma unroll
-              for (int j = 0; j < 16; ++j) fma2(acc[g * 16 + j], r[2 * j], r[2 * j + 1], s2);
-            }
-            acc_buf ^= 1;
-            if (acc_buf == 0) acc_phase ^= 1;
           }
+          const float s = __fmul_rn(sm->xs[slot][i][quarter * 32 + lane], sm->ws[slot][i][half]);
+          if (i == kScaleKb - 1 || kb == nkb - 1) {
+            __syncwarp();
+            if (lane == 0) mbar_arrive(&sm->sempty[slot]);
+            if (++slot == kScaleSlots) {
+              slot = 0;
+              slot_phase ^= 1;
+            }
+          }
+          if (!wait_bar(my_tfull + 8 * C::kHalves * acc_buf, acc_phase, abort_flag, args.status, args.timeout_ns)) {
+            ok = false;
+            break;
+          }
+          tc_fence_after();
+          // 32 columns are in flight while the 32 before them are added.
+          uint32_t r[2][32];
+          tmem_ld_32cols(t_lane + acc_buf * kBN, r[0]);
+#pragma unroll
+          for (int g = 0; g < kNC / 32; ++g) {
+            tmem_ld_wait();
+            if (g + 1 < kNC / 32)
+              tmem_ld_32cols(t_lane + acc_buf * kBN + (g + 1) * 32, r[(g + 1) & 1]);
+            else
+              release(acc_buf);
+#pragma unroll
+            for (int j = 0; j < 32; ++j) acc[g * 32 + j] = fmaf(__uint_as_float(r[g & 1][j]), s, acc[g * 32 + j]);
+          }
+          acc_buf ^= 1;
+          if (acc_buf == 0) acc_phase ^= 1;
         }
         if (!ok) break;
-        if (row_ok) {
 #pragma unroll
-          for (int c = 0; c < kNC / 8; ++c) {
-            float x[8];
-#pragma unroll
-            for (int j = 0; j < 4; ++j) unpack2(acc[c * 4 + j], x[2 * j], x[2 * j + 1]);
-            store8(args, row, col0 + c * 8, x);
-          }
-        }
+        for (int g = 0; g < kNC / 32; ++g)
+          store_cols32(args, out_buf, row0, u.r1, col0 + g * 32, lane, reinterpret_cast<float(&)[32]>(acc[g * 32]));
       } else {
-        if (!mbar_wait<kPair>(&sm->tfull[acc_buf], acc_phase, abort_flag, args.status, args.timeout_ns, false)) break;
+        if (!wait_bar(my_tfull + 8 * C::kHalves * acc_buf, acc_phase, abort_flag, args.status, args.timeout_ns)) break;
         tc_fence_after();
 #pragma unroll 1
         for (int g = 0; g < kNC / 32; ++g) {
           uint32_t r[32];
-          __syncwarp();
           tmem_ld_32cols(t_lane + acc_buf * kBN + g * 32, r);
           tmem_ld_wait();
           if (g == kNC / 32 - 1) release(acc_buf);
-          if (!row_ok) continue;
+          float x[32];
 #pragma unroll
-          for (int c = 0; c < 4; ++c) {
-            float x[8];
-#pragma unroll
-            for (int j = 0; j < 8; ++j) x[j] = __uint_as_float(r[c * 8 + j]);
-            store8(args, row, col0 + g * 32 + c * 8, x);
-          }
+          for (int j = 0; j < 32; ++j) x[j] = __uint_as_float(r[j]);
+          store_cols32(args, out_buf, row0, u.r1, col0 + g * 32, lane, x);
         }
         acc_buf ^= 1;
         if (acc_buf == 0) acc_phase ^= 1;
@@ -660,7 +837,7 @@ cudaError_t device_info(DeviceInfo* d) {
 
 template <bool kF8, bool kPair, int kBN>
 cudaError_t launch_tile(const ProductArgs& a, const DeviceInfo& d, cudaStream_t st) {
-  using C = TileCfg<kPair, kBN>;
+  using C = TileCfg<kF8, kPair, kBN>;
   auto* fn = tile_kernel<kF8, kPair, kBN>;
   // Per kernel and device: the resident units (CTAs or pairs), once its
   // shared-memory limit is raised.  0: not yet done.
@@ -697,10 +874,10 @@ cudaError_t launch_tile(const ProductArgs& a, const DeviceInfo& d, cudaStream_t 
   const uint64_t bytes = static_cast<uint64_t>(a.in) * (kF8 ? 1 : 2);
   const uint64_t w_rows = static_cast<uint64_t>(a.experts) * a.out;
   cudaError_t e = make_tmap_bytes(&mx, a.X, a.n, bytes, a.ldx, kRowTile);
-  if (e == cudaSuccess) e = make_tmap_bytes(&mw, a.W, w_rows, bytes, a.ldw, C::kBRows);
+  if (e == cudaSuccess) e = make_tmap_bytes(&mw, a.W, w_rows, bytes, a.ldw, C::kBRows / C::kWBoxes);
   if (e != cudaSuccess) return e;
   mlo = mw;
-  if (a.W_lo) e = make_tmap_bytes(&mlo, a.W_lo, w_rows, bytes, a.ldw, C::kBRows);
+  if (a.W_lo) e = make_tmap_bytes(&mlo, a.W_lo, w_rows, bytes, a.ldw, C::kBRows / C::kWBoxes);
   if (e != cudaSuccess) return e;
   cfg.gridDim = dim3(static_cast<unsigned>(kPair ? 2 * units : units));
   return cudaLaunchKernelEx(&cfg, fn, mx, mw, mlo, a);
@@ -719,6 +896,10 @@ cudaError_t launch_type(const ProductArgs& a, const DeviceInfo& d, cudaStream_t 
       skinny_kernel<kF8, 4><<<grid, 32 * kSkinnyWarps, 0, st>>>(a);
     return cudaGetLastError();
   }
+  const char* ev = getenv("AR_TILE");
+  const int tv = ev ? atoi(ev) : 0;
+  if (tv == 2) return launch_tile<kF8, true, 256>(a, d, st);
+  if (tv == 1) return launch_tile<kF8, false, 256>(a, d, st);
   return launch_tile<kF8, false, 128>(a, d, st);
 }
 
