@@ -1,9 +1,11 @@
 """Python binding of libar: AutoRound per-layer SignSGD tuning on one B200.
 
 Argument marshalling only: every step of the computation runs in libar's CUDA
-kernels (``libar.so``, built in-tree by ``python signed_gradient_rounding_b200/build.py``).
-PyTorch provides device memory and streams.  Importing this package fails
-loudly when the library is missing; there is no CPU fallback.
+kernels (``libar.so``, built in-tree by ``python signed_gradient_rounding_b200/build.py``);
+the entry points that also run for single tokens are marshalled by a compiled module
+(``_binding.so``, built with it), the others through ctypes.  PyTorch provides device
+memory and streams.  Importing this package fails loudly when the library is missing;
+there is no CPU fallback.
 
 Entry points (same names as the C ABI in include/ar.h):
   rtn, fake_quant, pack, tune_workspace_bytes, tune_layer, tune_status,
@@ -143,6 +145,8 @@ def _load() -> ctypes.CDLL:
 _lib = _load()
 lib = _lib
 
+from . import _binding  # noqa: E402  (built beside libar.so, which it links)
+
 
 def version() -> str:
     return _lib.ar_version().decode()
@@ -271,78 +275,12 @@ def silu_mul(a: torch.Tensor, b: torch.Tensor, stream=None) -> torch.Tensor:
 # [rows, ceil(cols/128)] for activations or [ceil(rows/128), ceil(cols/128)] for
 # weights).  Tensors may have a row pitch (a slice of wider rows); their columns are
 # contiguous.  Calls run on the tensors' device, on its current stream by default.
+# Checks, output allocation and the call itself are in the compiled _binding module;
+# a refused argument raises ValueError, a status of the library ArError.
 # ---------------------------------------------------------------------------
 
 SCALE_BLOCK = 128
-_E4M3 = torch.float8_e4m3fn
-_DTYPES = {torch.float32: AR_F32, torch.bfloat16: AR_BF16}
-
-
-def _rows(t: torch.Tensor, name: str, dev: int, dtype: torch.dtype | None = None, shape=None) -> int:
-    """Row pitch (elements) of a CUDA matrix on device ``dev``; checks its dtype and shape."""
-    if t.get_device() != dev or dev < 0:
-        raise ValueError(f"{name} must be a CUDA tensor" + ("" if dev < 0 else f" on cuda:{dev}"))
-    if dtype is not None and t.dtype != dtype:
-        raise ValueError(f"{name} must be {dtype}")
-    size = t.shape
-    if len(size) != 2 or (shape is not None and size != shape):
-        raise ValueError(f"{name} must be {list(shape) if shape is not None else 'a matrix'}, got {list(size)}")
-    rows, cols = size
-    pitch, step = t.stride()
-    if cols > 1 and step != 1:
-        raise ValueError(f"{name} must have contiguous columns")
-    return pitch if rows > 1 else cols
-
-
-def _flat(t: torch.Tensor, name: str, dev: int, dtype: torch.dtype, shape) -> int:
-    """Pointer of a contiguous CUDA tensor on device ``dev`` with this dtype and shape."""
-    if t.get_device() != dev:
-        raise ValueError(f"{name} must be a CUDA tensor on cuda:{dev}")
-    if t.dtype != dtype or t.shape != shape or not t.is_contiguous():
-        raise ValueError(f"{name} must be a contiguous {dtype} tensor {list(shape)}, got {t.dtype} {list(t.shape)}")
-    return t.data_ptr()
-
-
-def _experts(t: torch.Tensor, name: str, dev: int, dtype: torch.dtype) -> int:
-    """Row pitch of expert weights [experts, out, in] whose matrices follow one another."""
-    if t.get_device() != dev:
-        raise ValueError(f"{name} must be a CUDA tensor on cuda:{dev}")
-    if t.dtype != dtype or t.dim() != 3:
-        raise ValueError(f"{name} must be {dtype} [experts, out, in]")
-    e, out, inn = t.shape
-    se, pitch, step = t.stride()
-    if (inn > 1 and step != 1) or (e > 1 and se != (pitch if out > 1 else inn) * out):
-        raise ValueError(f"{name} must have contiguous rows, and matrices that follow one another")
-    return pitch if out > 1 else inn
-
-
-def _status(t: torch.Tensor | None, dev: int):
-    """Pointer of an optional int32 status word on device ``dev``."""
-    if t is None:
-        return None
-    if t.get_device() != dev or t.dtype != torch.int32 or t.numel() < 1:
-        raise ValueError(f"status must be an int32 CUDA tensor on cuda:{dev} with an element")
-    return t.data_ptr()
-
-
-def _launch(fn, what: str, dev: int, stream, *args) -> None:
-    """Call ``fn(*args, stream)`` with device ``dev`` current."""
-    if stream is None:
-        stream = torch.cuda.current_stream(dev)
-    if torch.cuda.current_device() == dev:
-        status = fn(*args, stream.cuda_stream)
-    else:
-        with torch.cuda.device(dev):
-            status = fn(*args, stream.cuda_stream)
-    if status != AR_OK:
-        raise ArError(status, what)
-
-
-def _dt(t: torch.Tensor, name: str) -> int:
-    d = _DTYPES.get(t.dtype)
-    if d is None:
-        raise ValueError(f"{name} must be float32 or bfloat16")
-    return d
+_binding.set_error_type(ArError)
 
 
 def rms_norm(x: torch.Tensor, weight: torch.Tensor | None, eps: float = 1e-6, residual: torch.Tensor | None = None,
@@ -350,97 +288,25 @@ def rms_norm(x: torch.Tensor, weight: torch.Tensor | None, eps: float = 1e-6, re
     """h = x + residual, v = h / sqrt(mean(h^2) + eps) * weight: (v bf16 or None, q, scale of v as a
     scaled tensor or None, h in the residual's dtype or None without one).  ``sum_out`` may be the
     residual itself (updated in place)."""
-    dev = x.get_device()
-    ldx = _rows(x, "x", dev)
-    shape = x.shape
-    rows, cols = shape
-    xd = _dt(x, "x")
-    rp, rd, ldr, h, lds = None, xd, cols, None, cols
-    if residual is not None:
-        ldr, rd, rp = _rows(residual, "residual", dev, None, shape), _dt(residual, "residual"), residual.data_ptr()
-        h = sum_out
-        if h is None:
-            h = torch.empty(shape, dtype=residual.dtype, device=x.device)
-            lds = cols
-        else:
-            lds = _rows(h, "sum_out", dev, residual.dtype, shape)
-    elif sum_out is not None:
-        raise ValueError("sum_out needs a residual")
-    wp, wd = None, AR_BF16
-    if weight is not None:
-        wd = _dt(weight, "weight")
-        wp = _flat(weight, "weight", dev, weight.dtype, (cols,))
-    y = torch.empty(shape, dtype=torch.bfloat16, device=x.device) if want_bf16 else None
-    q = scale = None
-    if want_scaled:
-        q = torch.empty(shape, dtype=_E4M3, device=x.device)
-        scale = torch.empty((rows, (cols + 127) // 128), dtype=torch.float32, device=x.device)
-    _launch(_lib.ar_rms_norm, "ar_rms_norm", dev, stream, x.data_ptr(), xd, ldx, rows, cols, rp, rd, ldr, wp, wd, eps,
-            None if h is None else h.data_ptr(), lds, None if y is None else y.data_ptr(), cols,
-            None if q is None else q.data_ptr(), cols, None if scale is None else scale.data_ptr())
-    return y, q, scale, h
+    return _binding.rms_norm(x, weight, eps, residual, want_bf16, want_scaled, sum_out, stream)
 
 
 def quant_scaled(x: torch.Tensor, block_rows: int = 1, stream=None):
     """(q, scale) of a matrix, or of a stack of matrices [count, rows, cols], fp32 or bf16:
     block_rows 1 for activations, 128 for weights."""
-    dev = x.get_device()
-    xd = _dt(x, "x")
-    if x.dim() == 3:
-        count, rows, cols = x.shape
-        ldx = _experts(x, "x", dev, x.dtype)
-    else:
-        ldx = _rows(x, "x", dev)
-        count, (rows, cols) = 1, x.shape
-    blocks = (cols + 127) // 128
-    row_blocks = rows if block_rows == 1 else (rows + 127) // 128
-    q = torch.empty(x.shape, dtype=_E4M3, device=x.device)
-    scale = torch.empty((count, row_blocks, blocks) if x.dim() == 3 else (row_blocks, blocks), dtype=torch.float32,
-                        device=x.device)
-    _launch(_lib.ar_quant_scaled, "ar_quant_scaled", dev, stream, x.data_ptr(), xd, ldx, count, rows, cols, block_rows,
-            q.data_ptr(), cols, scale.data_ptr())
-    return q, scale
+    return _binding.quant_scaled(x, block_rows, stream)
 
 
 def silu_mul_scaled(a: torch.Tensor, b: torch.Tensor, stream=None):
     """silu(a) * b (bf16 matrices) as a scaled tensor (q, scale) with row blocks."""
-    dev = a.get_device()
-    shape = a.shape
-    lda = _rows(a, "a", dev, torch.bfloat16)
-    ldb = _rows(b, "b", dev, torch.bfloat16, shape)
-    rows, cols = shape
-    q = torch.empty(shape, dtype=_E4M3, device=a.device)
-    scale = torch.empty((rows, (cols + 127) // 128), dtype=torch.float32, device=a.device)
-    _launch(_lib.ar_silu_mul_scaled, "ar_silu_mul_scaled", dev, stream, a.data_ptr(), lda, b.data_ptr(), ldb, rows, cols,
-            q.data_ptr(), cols, scale.data_ptr())
-    return q, scale
+    return _binding.silu_mul_scaled(a, b, stream)
 
 
 def linear_scaled(Xq: torch.Tensor, x_scale: torch.Tensor, Wq: torch.Tensor, w_scale: torch.Tensor,
                   add: torch.Tensor | None = None, out: torch.Tensor | None = None, status: torch.Tensor | None = None,
                   stream=None) -> torch.Tensor:
     """bf16(X W^T + add) of scaled tensors X [n, in] (row blocks) and W [out, in] (128 x 128 blocks)."""
-    dev = Xq.get_device()
-    ldx = _rows(Xq, "Xq", dev, _E4M3)
-    ldw = _rows(Wq, "Wq", dev, _E4M3)
-    n, inn = Xq.shape
-    o, win = Wq.shape
-    if win != inn:
-        raise ValueError(f"Wq must be [out, {inn}]")
-    nb = (inn + 127) // 128
-    xs = _flat(x_scale, "x_scale", dev, torch.float32, (n, nb))
-    ws = _flat(w_scale, "w_scale", dev, torch.float32, ((o + 127) // 128, nb))
-    ap, lda = None, o
-    if add is not None:
-        lda, ap = _rows(add, "add", dev, torch.bfloat16, (n, o)), add.data_ptr()
-    if out is None:
-        out = torch.empty((n, o), dtype=torch.bfloat16, device=Xq.device)
-        ldy = o
-    else:
-        ldy = _rows(out, "out", dev, torch.bfloat16, (n, o))
-    _launch(_lib.ar_linear_scaled, "ar_linear_scaled", dev, stream, Xq.data_ptr(), ldx, xs, n, inn, Wq.data_ptr(), ldw,
-            ws, o, ap, lda, out.data_ptr(), ldy, _status(status, dev))
-    return out
+    return _binding.linear_scaled(Xq, x_scale, Wq, w_scale, add, out, status, stream)
 
 
 def grouped_linear(X: torch.Tensor, offsets: torch.Tensor, W_hi: torch.Tensor, W_lo: torch.Tensor | None = None,
@@ -448,27 +314,7 @@ def grouped_linear(X: torch.Tensor, offsets: torch.Tensor, W_hi: torch.Tensor, W
     """Y[r] = bf16(X[r] (W_hi[e] + W_lo[e])^T) for the rows offsets[e] <= r < offsets[e+1] of expert e:
     X [n, in] bf16, W [experts, out, in] bf16, offsets int32 [experts + 1] on the device.  Rows outside
     the experts' are left as they are in ``out`` (and undefined in a new tensor)."""
-    dev = X.get_device()
-    ldx = _rows(X, "X", dev, torch.bfloat16)
-    ldw = _experts(W_hi, "W_hi", dev, torch.bfloat16)
-    n, inn = X.shape
-    e, o, win = W_hi.shape
-    if win != inn:
-        raise ValueError(f"W_hi must be [experts, out, {inn}]")
-    lo = None
-    if W_lo is not None:
-        if W_lo.shape != W_hi.shape or _experts(W_lo, "W_lo", dev, torch.bfloat16) != ldw:
-            raise ValueError("W_lo must have the shape and strides of W_hi")
-        lo = W_lo.data_ptr()
-    offs = _flat(offsets, "offsets", dev, torch.int32, (e + 1,))
-    if out is None:
-        out = torch.empty((n, o), dtype=torch.bfloat16, device=X.device)
-        ldy = o
-    else:
-        ldy = _rows(out, "out", dev, torch.bfloat16, (n, o))
-    _launch(_lib.ar_grouped_linear, "ar_grouped_linear", dev, stream, X.data_ptr(), ldx, n, inn, offs, e,
-            W_hi.data_ptr(), lo, ldw, o, out.data_ptr(), ldy, _status(status, dev))
-    return out
+    return _binding.grouped_linear(X, offsets, W_hi, W_lo, out, status, stream)
 
 
 def grouped_linear_scaled(Xq: torch.Tensor, x_scale: torch.Tensor, offsets: torch.Tensor, Wq: torch.Tensor,
@@ -476,25 +322,7 @@ def grouped_linear_scaled(Xq: torch.Tensor, x_scale: torch.Tensor, offsets: torc
                           stream=None) -> torch.Tensor:
     """grouped_linear of scaled tensors X [n, in] (row blocks) and W [experts, out, in] (128 x 128 blocks,
     w_scale [experts, ceil(out/128), ceil(in/128)])."""
-    dev = Xq.get_device()
-    ldx = _rows(Xq, "Xq", dev, _E4M3)
-    ldw = _experts(Wq, "Wq", dev, _E4M3)
-    n, inn = Xq.shape
-    e, o, win = Wq.shape
-    if win != inn:
-        raise ValueError(f"Wq must be [experts, out, {inn}]")
-    nb = (inn + 127) // 128
-    xs = _flat(x_scale, "x_scale", dev, torch.float32, (n, nb))
-    ws = _flat(w_scale, "w_scale", dev, torch.float32, (e, (o + 127) // 128, nb))
-    offs = _flat(offsets, "offsets", dev, torch.int32, (e + 1,))
-    if out is None:
-        out = torch.empty((n, o), dtype=torch.bfloat16, device=Xq.device)
-        ldy = o
-    else:
-        ldy = _rows(out, "out", dev, torch.bfloat16, (n, o))
-    _launch(_lib.ar_grouped_linear_scaled, "ar_grouped_linear_scaled", dev, stream, Xq.data_ptr(), ldx, xs, n, inn, offs,
-            e, Wq.data_ptr(), ldw, ws, o, out.data_ptr(), ldy, _status(status, dev))
-    return out
+    return _binding.grouped_linear_scaled(Xq, x_scale, offsets, Wq, w_scale, out, status, stream)
 
 
 def make_params(bits=4, group_size=128, sym=False, iters=200, lr=0.005, minmax_lr=-1.0, minmax_shrink=1.0,

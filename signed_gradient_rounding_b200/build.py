@@ -1,4 +1,5 @@
-"""Build libar.so (the CUDA kernels and the C ABI) in-tree for sm_100a.
+"""Build libar.so (the CUDA kernels and the C ABI) in-tree for sm_100a, and _binding.so,
+the compiled part of the Python binding (a torch extension that calls libar.so).
 
 Usage:  python signed_gradient_rounding_b200/build.py [--verbose]
 
@@ -19,6 +20,8 @@ ROOT = os.path.dirname(PKG)
 CSRC = os.path.join(PKG, "csrc")
 SOURCES = ["api.cu", "quant_kernels.cu", "gemm_sm100.cu", "scaled_rows.cu", "scaled_product.cu", "scaled_api.cu"]
 LIB = os.path.join(PKG, "libar.so")
+BINDING_SRC = os.path.join(CSRC, "binding.cpp")
+BINDING = os.path.join(PKG, "_binding.so")
 
 NVCC_FLAGS = [
     "-O3", "-std=c++17", "-lineinfo",
@@ -36,12 +39,33 @@ def nvcc() -> str:
 
 
 def _stale() -> bool:
-    if not os.path.exists(LIB):
+    if not os.path.exists(LIB) or not os.path.exists(BINDING):
         return True
-    t = os.path.getmtime(LIB)
+    t = min(os.path.getmtime(LIB), os.path.getmtime(BINDING))
     deps = [os.path.join(CSRC, f) for f in os.listdir(CSRC)] + [os.path.join(ROOT, "include", "ar.h"),
                                                                 os.path.abspath(__file__)]
     return any(os.path.getmtime(d) > t for d in deps if os.path.exists(d))
+
+
+def _build_binding(verbose: bool) -> None:
+    """The torch extension; it finds libar.so beside itself ($ORIGIN)."""
+    import sysconfig
+
+    import torch
+    from torch.utils.cpp_extension import include_paths, library_paths
+    incs = [*include_paths(), sysconfig.get_paths()["include"], os.path.join(os.path.dirname(os.path.dirname(nvcc())),
+                                                                             "include")]
+    tmp = BINDING + ".tmp"
+    cmd = [os.environ.get("CXX", "g++"), "-O2", "-std=c++17", "-fPIC", "-shared", "-fvisibility=hidden",
+           f"-D_GLIBCXX_USE_CXX11_ABI={int(torch._C._GLIBCXX_USE_CXX11_ABI)}", BINDING_SRC, "-o", tmp]
+    cmd += [x for i in incs for x in ("-isystem", i)]
+    cmd += [f"-L{p}" for p in (*library_paths(), PKG)]
+    cmd += ["-l:libar.so", "-ltorch_python", "-ltorch", "-ltorch_cpu", "-ltorch_cuda", "-lc10", "-lc10_cuda",
+            "-Wl,-rpath,$ORIGIN"]
+    if verbose:
+        print(" ".join(cmd), flush=True)
+    subprocess.run(cmd, check=True)
+    os.replace(tmp, BINDING)
 
 
 def build(force: bool = False, verbose: bool = False) -> str:
@@ -62,6 +86,7 @@ def build(force: bool = False, verbose: bool = False) -> str:
     os.replace(tmp, LIB)
     for o in objs:
         os.remove(o)
+    _build_binding(verbose)
     return LIB
 
 
