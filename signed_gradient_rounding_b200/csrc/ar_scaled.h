@@ -80,6 +80,7 @@ struct ProductArgs {
   uint16_t* Y = nullptr;             // [n, out] bf16, pitch ldy
   int64_t ldy = 0;
   int vec_y = 0;                     // Y and add take 16-byte accesses at multiples of 8 columns
+  int split = 1;                     // CTAs of a cluster that share K (set by the launch)
   int* status = nullptr;
   uint64_t timeout_ns = 1000000000ull;
 };

@@ -58,7 +58,7 @@ constexpr int kScaleSlots = 4;
 
 struct TileSmem {
   uint64_t full[kMaxStages], empty[kMaxStages];
-  uint64_t tfull[4], tempty[4];  // accumulator b of column half h: 2 b + h (one half: b)
+  uint64_t tfull[4], tempty[4];  // accumulator b of column half h: kHalves b + h
   uint64_t sfull[kScaleSlots], sempty[kScaleSlots];
   uint64_t drain[2];
   uint32_t tmem_base;
@@ -66,7 +66,6 @@ struct TileSmem {
   // e4m3: scales of kScaleKb K blocks per slot, of the CTA's rows and column halves
   float xs[kScaleSlots][kScaleKb][kRowTile];
   float ws[kScaleSlots][kScaleKb][2];
-  uint4 out[8][128];         // per epilogue warp: 32 rows x 32 columns of Y
   int cum[kMaxExperts + 1];  // row blocks of the experts before e
 };
 
@@ -81,13 +80,19 @@ struct TileCfg {
   static constexpr int kWBoxes = kPair ? kHalves : 1;   // ... in so many loads (a pair's half: 64 rows in each CTA)
   static constexpr int kABytes = kRowTile * kKBytes;
   static constexpr int kStageBytes = kABytes + kBRows * kKBytes;
-  static constexpr int kStages = kStageBytes <= 32768 ? 6 : 4;
+  static constexpr int kStages = kBN == 128 ? 5 : kPair ? 4 : 3;
+  static constexpr int kNC = kBN / 2;               // columns per epilogue thread
+  static constexpr int kRowPitch = kNC * 2 + 16;    // a row's part of Y on its way out; + 16: no bank conflicts
+  static constexpr int kAccs = 512 / kBN;           // accumulators in tensor memory
   static constexpr int kBM = kPair ? 2 * kRowTile : kRowTile;  // rows per unit (CTA or pair)
-  static constexpr int kTmemCols = 2 * kBN;                    // two accumulators
-  static constexpr int kBarOffset = kStages * kStageBytes;
+  static constexpr int kTmemCols = 512;
+  static constexpr int kOutOffset = kStages * kStageBytes;
+  static constexpr int kBarOffset = kOutOffset + 8 * 32 * kRowPitch;
   static constexpr int kSmemBytes = 1024 + kBarOffset + static_cast<int>(sizeof(TileSmem));
   static_assert(kSmemBytes <= 232448, "shared memory per CTA");
-  static_assert(kTmemCols <= 512, "tensor memory");
+  static_assert(kAccs * kHalves <= 4, "accumulator barriers");
+  // the shares of a split K, 128 x 128 fp32, pass through the operand stages
+  static_assert(kBN != 128 || kStages * kStageBytes >= 128 * 128 * 4, "split-K exchange");
 };
 
 struct Unit {
@@ -161,58 +166,74 @@ __device__ __forceinline__ void store8(const ProductArgs& a, int64_t row, int co
   }
 }
 
-// Columns [col, col + 32) of a warp's 32 rows (row0 ..; those from r1 on belong to others),
-// lane = row, x the lane's values.  Through shared memory, so that a store instruction
-// writes 64 contiguous bytes of 8 rows: stored from where they are, 16 bytes of 32 rows at
-// a time, the columns of a 256 x 256 tile took 7500 cycles.  The buffer's 16-byte units are
-// swizzled by the row pair: no bank conflicts either way.
-__device__ __forceinline__ void store_cols32(const ProductArgs& a, uint4* buf, int row0, int r1, int col, int lane,
-                                             float (&x)[32]) {
-  if (row0 >= r1 || col >= a.out) return;  // the whole warp
-  if (!a.vec_y || col + 32 > a.out) {
-    if (row0 + lane < r1) {
+// The way out of a warp's 32 rows x kNC columns (lane = row; rows from r1 on belong to
+// others): each lane rounds its row's values into its own line of shared memory (put8) and
+// sends the line to Y with one bulk copy (send), which runs while the warp goes on with the
+// next unit.  (Stored from registers, 16 bytes of 32 rows per instruction, the columns of a
+// 256 x 256 tile kept the warps for 7500 cycles; through shared memory with coalesced
+// stores for 3700, since every SM writes at the same time.)
+template <int kNC>
+struct RowsOut {
+  uint8_t* line;    // this lane's line
+  int row, r1, col; // this lane's row; first column
+  int cols;         // columns that exist, at most kNC
+  bool bulk;        // whole 16-byte units at aligned addresses: the bulk copy; else direct stores
+
+  __device__ __forceinline__ void begin(const ProductArgs& a, uint8_t* warp_buf, int row0, int r1_, int col_, int lane) {
+    constexpr int kPitch = kNC * 2 + 16;
+    line = warp_buf + lane * kPitch;
+    row = row0 + lane;
+    r1 = r1_;
+    col = col_;
+    cols = min(kNC, a.out - col);
+    bulk = a.vec_y && cols % 8 == 0;
+    asm volatile("cp.async.bulk.wait_group.read 0;" ::: "memory");  // the last unit's copy has read the line
+    __syncwarp();  // (every lane's: the residual is brought in by the whole warp)
+    if (a.add && bulk) {
+      // the residual, coalesced, into the lines
+      constexpr int kUnits = kNC / 8;  // 16-byte units per row
+      const int unit = lane % kUnits;
 #pragma unroll
-      for (int c = 0; c < 4; ++c) store8(a, row0 + lane, col + c * 8, reinterpret_cast<float(&)[8]>(x[c * 8]));
+      for (int i = 0; i < kUnits; ++i) {
+        const int r = i * (32 / kUnits) + lane / kUnits;
+        if (row0 + r < r1 && unit * 8 < cols)
+          *reinterpret_cast<uint4*>(warp_buf + r * kPitch + unit * 16) =
+              *reinterpret_cast<const uint4*>(a.add + static_cast<int64_t>(row0 + r) * a.ldadd + col + unit * 8);
+      }
+      __syncwarp();
     }
-    return;
   }
-  const int r = lane >> 2, unit = lane & 3;  // of the coalesced side: rows r + 8 i
-  const int own = lane * 4, own_swz = (lane >> 1) & 3;
-  if (a.add) {
-#pragma unroll
-    for (int i = 0; i < 4; ++i) {
-      const int rr = r + 8 * i;
-      if (row0 + rr < r1)
-        buf[rr * 4 + (unit ^ ((rr >> 1) & 3))] =
-            *reinterpret_cast<const uint4*>(a.add + static_cast<int64_t>(row0 + rr) * a.ldadd + col + unit * 8);
+
+  __device__ __forceinline__ void put8(const ProductArgs& a, int c, float (&x)[8]) {
+    if (row >= r1) return;
+    if (!bulk) {
+      store8(a, row, col + c, x);
+      return;
     }
-    __syncwarp();
-#pragma unroll
-    for (int c = 0; c < 4; ++c) {
-      const uint4 v = buf[own + (c ^ own_swz)];
+    uint4* p = reinterpret_cast<uint4*>(line + c * 2);
+    if (a.add) {
+      const uint4 v = *p;
       const uint32_t w[4] = {v.x, v.y, v.z, v.w};
 #pragma unroll
       for (int j = 0; j < 4; ++j) {
-        x[c * 8 + 2 * j] += __uint_as_float(w[j] << 16);
-        x[c * 8 + 2 * j + 1] += __uint_as_float(w[j] & 0xFFFF0000u);
+        x[2 * j] += __uint_as_float(w[j] << 16);
+        x[2 * j + 1] += __uint_as_float(w[j] & 0xFFFF0000u);
       }
     }
-    __syncwarp();
+    *p = make_uint4(pack2(x[0], x[1]), pack2(x[2], x[3]), pack2(x[4], x[5]), pack2(x[6], x[7]));
   }
-#pragma unroll
-  for (int c = 0; c < 4; ++c)
-    buf[own + (c ^ own_swz)] = make_uint4(pack2(x[c * 8], x[c * 8 + 1]), pack2(x[c * 8 + 2], x[c * 8 + 3]),
-                                          pack2(x[c * 8 + 4], x[c * 8 + 5]), pack2(x[c * 8 + 6], x[c * 8 + 7]));
-  __syncwarp();
-#pragma unroll
-  for (int i = 0; i < 4; ++i) {
-    const int rr = r + 8 * i;
-    if (row0 + rr < r1)
-      *reinterpret_cast<uint4*>(a.Y + static_cast<int64_t>(row0 + rr) * a.ldy + col + unit * 8) =
-          buf[rr * 4 + (unit ^ ((rr >> 1) & 3))];
+
+  __device__ __forceinline__ void send(const ProductArgs& a) {
+    if (bulk && row < r1 && cols > 0) {
+      asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
+      asm volatile("cp.async.bulk.global.shared::cta.bulk_group [%0], [%1], %2;" ::"l"(
+                       a.Y + static_cast<int64_t>(row) * a.ldy + col),
+                   "r"(smem_u32(line)), "r"(cols * 2)
+                   : "memory");
+    }
+    asm volatile("cp.async.bulk.commit_group;" ::: "memory");
   }
-  __syncwarp();
-}
+};
 
 // tcgen05 and TMA instructions issued by the whole warp with a predicate that holds in
 // one lane (elect_one).  In a branch of one lane the compiler can neither keep their
@@ -285,6 +306,15 @@ __device__ __forceinline__ void tma_load_if(uint32_t leader, uint32_t dst, const
         : "memory");
 }
 
+__device__ __forceinline__ float4 ld_cluster(uint32_t addr) {
+  float4 v;
+  asm volatile("ld.shared::cluster.v4.f32 {%0, %1, %2, %3}, [%4];"
+               : "=f"(v.x), "=f"(v.y), "=f"(v.z), "=f"(v.w)
+               : "r"(addr)
+               : "memory");
+  return v;
+}
+
 // Wait for the phase of `bar` with this parity (whole warps).  After timeout_ns, or once
 // another role has given up (*abort), it records kDevTimeout in *status, raises *abort and
 // returns false.  The test is one instruction of the warp, so its lanes leave together.
@@ -349,14 +379,17 @@ __global__ void __launch_bounds__(kTileThreads, 1)
   volatile int* abort_flag = &sm->abort_flag;
   const int warp = __shfl_sync(0xffffffffu, static_cast<int>(threadIdx.x >> 5), 0);  // warp-uniform
   const int lane = threadIdx.x & 31;
-  const uint32_t rank = kPair ? cluster_ctarank() : 0u;
+  // A cluster is a pair of CTAs that share a 256-row tile, or args.split CTAs that share K.
+  const bool split = !kPair && args.split > 1;
+  const uint32_t cta = kPair || split ? cluster_ctarank() : 0u;
+  const uint32_t rank = kPair ? cta : 0u;
 
   if (warp == 1 && lane == 0) {
     for (int s = 0; s < C::kStages; ++s) {
       mbar_init(&sm->full[s], 1);
       mbar_init(&sm->empty[s], C::kHalves);  // one commit per issuer
     }
-    for (int b = 0; b < 2 * C::kHalves; ++b) {
+    for (int b = 0; b < C::kAccs * C::kHalves; ++b) {
       mbar_init(&sm->tfull[b], 1);
       mbar_init(&sm->tempty[b], (kPair ? 2 : 1) * 8 / C::kHalves);  // one arrive per epilogue warp that reads it
     }
@@ -417,10 +450,13 @@ __global__ void __launch_bounds__(kTileThreads, 1)
   const uint32_t tmem_base = sm->tmem_base;
   const int num_n = (args.out + kBN - 1) / kBN;
   const int64_t num_units = static_cast<int64_t>(sm->cum[args.experts]) * num_n;
-  const int64_t unit0 = kPair ? blockIdx.x >> 1 : blockIdx.x;
-  const int64_t stride = kPair ? gridDim.x >> 1 : gridDim.x;
+  const int64_t unit0 = kPair ? blockIdx.x >> 1 : split ? blockIdx.x / args.split : blockIdx.x;
+  const int64_t stride = kPair ? gridDim.x >> 1 : split ? num_units : gridDim.x;  // split: one unit per cluster
   const int nkb = args.nkb;
   const int k_total = (!kF8 && args.W_lo) ? 2 * nkb : nkb;
+  // This CTA's share of K (not empty: split <= nkb).
+  const int k_begin = split ? static_cast<int>(static_cast<int64_t>(k_total) * cta / args.split) : 0;
+  const int k_end = split ? static_cast<int>(static_cast<int64_t>(k_total) * (cta + 1) / args.split) : k_total;
   const uint32_t bar_full = smem_u32(sm->full), bar_empty = smem_u32(sm->empty);
   const uint32_t bar_tfull = smem_u32(sm->tfull), bar_tempty = smem_u32(sm->tempty);
 
@@ -438,7 +474,7 @@ __global__ void __launch_bounds__(kTileThreads, 1)
         const Unit u = find_unit(args, sm->cum, t, num_n, C::kBM, kBN);
         const int x_row = u.m0 + static_cast<int>(rank) * kRowTile;
         const int w_row = u.e * args.out + u.n0 + static_cast<int>(rank) * (C::kBRows / C::kWBoxes);
-        for (int kb = 0; kb < k_total; ++kb) {
+        for (int kb = k_begin; kb < k_end; ++kb) {
           if (!wait_bar(bar_empty + 8 * stage, phase ^ 1, abort_flag, args.status, args.timeout_ns)) {
             ok = false;
             break;
@@ -486,9 +522,9 @@ __global__ void __launch_bounds__(kTileThreads, 1)
         uint32_t phase = 0, acc_phase = 0;
         bool ok = true;
         for (int64_t t = unit0; ok && t < num_units; t += stride) {
-          for (int kb = 0; kb < k_total; ++kb) {
+          for (int kb = k_begin; kb < k_end; ++kb) {
             const uint32_t bar_acc = 8 * (acc * C::kHalves + half);
-            const bool first = kF8 || kb == 0, last = kF8 || kb == k_total - 1;
+            const bool first = kF8 || kb == k_begin, last = kF8 || kb == k_end - 1;
             // both tests in flight at once: each takes over 100 cycles, passed or not
             const bool free = !first || mbar_try_wait(bar_tempty + bar_acc, acc_phase ^ 1);
             const bool here = mbar_try_wait(bar_full + 8 * stage, phase);
@@ -505,8 +541,10 @@ __global__ void __launch_bounds__(kTileThreads, 1)
             umma_commit_if<kPair>(leader, bar_empty + 8 * stage);
             if (last) {
               umma_commit_if<kPair>(leader, bar_tfull + bar_acc);
-              acc ^= 1;
-              if (acc == 0) acc_phase ^= 1;
+              if (++acc == C::kAccs) {
+                acc = 0;
+                acc_phase ^= 1;
+              }
             }
             if (++stage == C::kStages) {
               stage = 0;
@@ -542,7 +580,7 @@ __global__ void __launch_bounds__(kTileThreads, 1)
         // threads 0 .. 7 also bring the weight's scales: block lane / 2 of half lane % 2
         const int nb = min((u.n0 + (lane & 1) * (kBN / 2)) >> 7, args.out_blocks - 1);
         const float* w = args.ws + (static_cast<int64_t>(u.e) * args.out_blocks + nb) * nkb;
-        for (int kb0 = 0; kb0 < nkb; kb0 += kScaleKb) {
+        for (int kb0 = k_begin; kb0 < k_end; kb0 += kScaleKb) {
           if (!wait_bar(smem_u32(&sm->sempty[slot]), phase ^ 1, abort_flag, args.status, args.timeout_ns)) {
             ok = false;
             break;
@@ -563,14 +601,19 @@ __global__ void __launch_bounds__(kTileThreads, 1)
       }
       asm volatile("cp.async.wait_all;" ::: "memory");
     }
+    if (split) {
+      __syncwarp();
+      cluster_sync_all();
+      cluster_sync_all();
+    }
   } else {
     asm volatile("setmaxnreg.inc.sync.aligned.u32 224;");
     // -------------------------------------------------------------- epilogue
-    constexpr int kNC = kBN / 2;       // columns per thread
+    constexpr int kNC = C::kNC;
     const int quarter = warp & 3;      // tensor-memory lanes this warp may access
     const int half = (warp - kEpiWarp0) >> 2;  // column half of the tile
     const uint32_t t_lane = tmem_base + (static_cast<uint32_t>(quarter * 32) << 16) + half * kNC;
-    uint4* out_buf = sm->out[warp - kEpiWarp0];
+    uint8_t* out_buf = smem + C::kOutOffset + (warp - kEpiWarp0) * 32 * C::kRowPitch;
     // This warp's accumulator barriers (the empty one is the pair leader's): + 8 kHalves for the second buffer.
     const uint32_t my_tfull = bar_tfull + (C::kHalves == 2 ? 8 * half : 0);
     const uint32_t my_tempty =
@@ -592,8 +635,8 @@ __global__ void __launch_bounds__(kTileThreads, 1)
 #pragma unroll
         for (int i = 0; i < kNC; ++i) acc[i] = 0.f;
 #pragma unroll 1
-        for (int kb = 0; kb < nkb; ++kb) {
-          const int i = kb % kScaleKb;
+        for (int kb = k_begin; kb < k_end; ++kb) {
+          const int i = (kb - k_begin) % kScaleKb;
           if (i == 0) {
             if (!wait_bar(smem_u32(&sm->sfull[slot]), slot_phase, abort_flag, args.status, args.timeout_ns)) {
               ok = false;
@@ -601,7 +644,7 @@ __global__ void __launch_bounds__(kTileThreads, 1)
             }
           }
           const float s = __fmul_rn(sm->xs[slot][i][quarter * 32 + lane], sm->ws[slot][i][half]);
-          if (i == kScaleKb - 1 || kb == nkb - 1) {
+          if (i == kScaleKb - 1 || kb == k_end - 1) {
             __syncwarp();
             if (lane == 0) mbar_arrive(&sm->sempty[slot]);
             if (++slot == kScaleSlots) {
@@ -627,30 +670,91 @@ __global__ void __launch_bounds__(kTileThreads, 1)
 #pragma unroll
             for (int j = 0; j < 32; ++j) acc[g * 32 + j] = fmaf(__uint_as_float(r[g & 1][j]), s, acc[g * 32 + j]);
           }
-          acc_buf ^= 1;
-          if (acc_buf == 0) acc_phase ^= 1;
+          if (++acc_buf == C::kAccs) {
+            acc_buf = 0;
+            acc_phase ^= 1;
+          }
         }
         if (!ok) break;
+        if (split) {
+          // This share's sums, for the exchange below: [column / 4][row], 16 bytes each.
+          float4* part = reinterpret_cast<float4*>(smem) + half * (kNC / 4) * kRowTile + quarter * 32 + lane;
 #pragma unroll
-        for (int g = 0; g < kNC / 32; ++g)
-          store_cols32(args, out_buf, row0, u.r1, col0 + g * 32, lane, reinterpret_cast<float(&)[32]>(acc[g * 32]));
+          for (int c = 0; c < kNC / 4; ++c)
+            part[c * kRowTile] = make_float4(acc[4 * c], acc[4 * c + 1], acc[4 * c + 2], acc[4 * c + 3]);
+          break;
+        }
+        RowsOut<kNC> rows_out;
+        rows_out.begin(args, out_buf, row0, u.r1, col0, lane);
+#pragma unroll
+        for (int c = 0; c < kNC; c += 8) {
+          float x[8];
+#pragma unroll
+          for (int j = 0; j < 8; ++j) x[j] = acc[c + j];
+          rows_out.put8(args, c, x);
+        }
+        rows_out.send(args);
       } else {
         if (!wait_bar(my_tfull + 8 * C::kHalves * acc_buf, acc_phase, abort_flag, args.status, args.timeout_ns)) break;
         tc_fence_after();
+        RowsOut<kNC> rows_out;
+        if (!split) rows_out.begin(args, out_buf, row0, u.r1, col0, lane);
 #pragma unroll 1
         for (int g = 0; g < kNC / 32; ++g) {
           uint32_t r[32];
           tmem_ld_32cols(t_lane + acc_buf * kBN + g * 32, r);
           tmem_ld_wait();
           if (g == kNC / 32 - 1) release(acc_buf);
-          float x[32];
+          if (split) {
+            float4* part =
+                reinterpret_cast<float4*>(smem) + (half * (kNC / 4) + g * 8) * kRowTile + quarter * 32 + lane;
 #pragma unroll
-          for (int j = 0; j < 32; ++j) x[j] = __uint_as_float(r[j]);
-          store_cols32(args, out_buf, row0, u.r1, col0 + g * 32, lane, x);
+            for (int c = 0; c < 8; ++c)
+              part[c * kRowTile] = make_float4(__uint_as_float(r[4 * c]), __uint_as_float(r[4 * c + 1]),
+                                               __uint_as_float(r[4 * c + 2]), __uint_as_float(r[4 * c + 3]));
+          } else {
+#pragma unroll
+            for (int c = 0; c < 32; c += 8) {
+              float x[8];
+#pragma unroll
+              for (int j = 0; j < 8; ++j) x[j] = __uint_as_float(r[c + j]);
+              rows_out.put8(args, g * 32 + c, x);
+            }
+          }
         }
-        acc_buf ^= 1;
-        if (acc_buf == 0) acc_phase ^= 1;
+        if (split) break;
+        rows_out.send(args);
+        if (++acc_buf == C::kAccs) {
+          acc_buf = 0;
+          acc_phase ^= 1;
+        }
       }
+    }
+    asm volatile("cp.async.bulk.wait_group 0;" ::: "memory");
+    if (split) {
+      // Every CTA of the cluster adds its columns of the tile over the shares, in order.
+      // (The operand stages are free: the accumulator's last hand-over follows every MMA.)
+      cluster_sync_all();
+      if (ok && unit0 < num_units) {
+        const Unit u = find_unit(args, sm->cum, unit0, num_n, C::kBM, kBN);
+        const int per = kBN / (2 * args.split);  // columns per thread: 32, 16 or 8
+        const int r = quarter * 32 + lane;
+        const int c0 = static_cast<int>(cta) * 2 * per + half * per;
+        if (u.m0 + r < u.r1) {
+          for (int c = c0; c < c0 + per; c += 8) {
+            float x[8];
+            for (int k = 0; k < args.split; ++k) {
+              const uint32_t p = mapa_shared(smem_u32(smem) + ((c / 4) * kRowTile + r) * 16, k);
+              const float4 a = ld_cluster(p), b = ld_cluster(p + kRowTile * 16);
+              const float v[8] = {a.x, a.y, a.z, a.w, b.x, b.y, b.z, b.w};
+#pragma unroll
+              for (int j = 0; j < 8; ++j) x[j] = k == 0 ? v[j] : __fadd_rn(x[j], v[j]);
+            }
+            store8(args, u.m0 + r, u.n0 + c, x);
+          }
+        }
+      }
+      cluster_sync_all();  // no CTA leaves while another reads its shares
     }
   }
 
@@ -835,8 +939,13 @@ cudaError_t device_info(DeviceInfo* d) {
   return cudaSuccess;
 }
 
+// Units of bm rows x bn columns that can have work (exact for one expert).
+int64_t units_at_most(const ProductArgs& a, int bm, int bn) {
+  return ((static_cast<int64_t>(a.n) + bm - 1) / bm + a.experts - 1) * ((a.out + bn - 1) / bn);
+}
+
 template <bool kF8, bool kPair, int kBN>
-cudaError_t launch_tile(const ProductArgs& a, const DeviceInfo& d, cudaStream_t st) {
+cudaError_t launch_tile(ProductArgs a, const DeviceInfo& d, cudaStream_t st, int split = 1) {
   using C = TileCfg<kF8, kPair, kBN>;
   auto* fn = tile_kernel<kF8, kPair, kBN>;
   // Per kernel and device: the resident units (CTAs or pairs), once its
@@ -868,8 +977,10 @@ cudaError_t launch_tile(const ProductArgs& a, const DeviceInfo& d, cudaStream_t 
     resident[d.dev].store(units, std::memory_order_relaxed);
   }
   // At most this many units have work; with offsets on the device the exact number is not known here.
-  const int64_t most = (static_cast<int64_t>(a.n) / C::kBM + (a.offsets ? a.experts : 1)) * ((a.out + kBN - 1) / kBN);
-  if (most < units) units = static_cast<int>(most);
+  const int64_t most = units_at_most(a, C::kBM, kBN);
+  while (split > a.nkb) split /= 2;
+  a.split = split;
+  if (most < units || split > 1) units = static_cast<int>(most);
   CUtensorMap mx, mw, mlo;
   const uint64_t bytes = static_cast<uint64_t>(a.in) * (kF8 ? 1 : 2);
   const uint64_t w_rows = static_cast<uint64_t>(a.experts) * a.out;
@@ -879,7 +990,9 @@ cudaError_t launch_tile(const ProductArgs& a, const DeviceInfo& d, cudaStream_t 
   mlo = mw;
   if (a.W_lo) e = make_tmap_bytes(&mlo, a.W_lo, w_rows, bytes, a.ldw, C::kBRows / C::kWBoxes);
   if (e != cudaSuccess) return e;
-  cfg.gridDim = dim3(static_cast<unsigned>(kPair ? 2 * units : units));
+  const int cluster = kPair ? 2 : split;
+  attr[0].val.clusterDim.x = cluster;
+  cfg.gridDim = dim3(static_cast<unsigned>(cluster * units));
   return cudaLaunchKernelEx(&cfg, fn, mx, mw, mlo, a);
 }
 
@@ -900,7 +1013,8 @@ cudaError_t launch_type(const ProductArgs& a, const DeviceInfo& d, cudaStream_t 
   const int tv = ev ? atoi(ev) : 0;
   if (tv == 2) return launch_tile<kF8, true, 256>(a, d, st);
   if (tv == 1) return launch_tile<kF8, false, 256>(a, d, st);
-  return launch_tile<kF8, false, 128>(a, d, st);
+  const char* es = getenv("AR_SPLIT");
+  return launch_tile<kF8, false, 128>(a, d, st, es ? atoi(es) : 1);
 }
 
 }  // namespace
