@@ -15,7 +15,9 @@
 //     swizzle, so both operand types share one pipeline.
 //   * skinny_kernel: few rows per expert, bound by the weight's bytes; each weight
 //     byte goes from HBM straight into the registers of the warp that multiplies it.
+#include <stddef.h>
 #include <stdlib.h>
+#include <string.h>
 
 #include <atomic>
 
@@ -63,8 +65,10 @@ struct TileSmem {
   uint64_t drain[2];
   uint32_t tmem_base;
   int abort_flag;
-  // e4m3: scales of kScaleKb K blocks per slot, of the CTA's rows and column halves
-  float xs[kScaleSlots][kScaleKb][kRowTile];
+  // e4m3: the scale ring.  A slot holds 16 bytes per row of the tile -- the aligned four of
+  // the row's scales, so the K block that a slot starts with differs from row to row by
+  // up to three -- and the weight's scales of four K blocks of each column half.
+  alignas(16) float xs[kScaleSlots][kRowTile][kScaleKb];
   float ws[kScaleSlots][kScaleKb][2];
   int cum[kMaxExperts + 1];  // row blocks of the experts before e
 };
@@ -90,6 +94,7 @@ struct TileCfg {
   static constexpr int kBarOffset = kOutOffset + 8 * 32 * kRowPitch;
   static constexpr int kSmemBytes = 1024 + kBarOffset + static_cast<int>(sizeof(TileSmem));
   static_assert(kSmemBytes <= 232448, "shared memory per CTA");
+  static_assert(kBarOffset % 16 == 0 && offsetof(TileSmem, xs) % 16 == 0, "16-byte asynchronous copies");
   static_assert(kAccs * kHalves <= 4, "accumulator barriers");
   // the shares of a split K, 128 x 128 fp32, pass through the operand stages
   static_assert(kBN != 128 || kStages * kStageBytes >= 128 * 128 * 4, "split-K exchange");
@@ -336,6 +341,15 @@ __device__ __forceinline__ bool wait_bar(uint32_t bar, uint32_t parity, volatile
   return true;
 }
 
+// Slots of the scale ring that a share of `blocks` K blocks takes (rows start up to three
+// blocks into their first).
+__device__ __forceinline__ int scale_slots(int blocks) { return (blocks + 3 + kScaleKb - 1) / kScaleKb; }
+
+// A 16-byte asynchronous copy of which the first `bytes` are read and the rest is zero.
+__device__ __forceinline__ void cp_async16(float* dst, const float* src, int bytes) {
+  asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(smem_u32(dst)), "l"(src), "r"(bytes) : "memory");
+}
+
 // A 4-byte asynchronous copy, and an arrive once the thread's copies so far are done.
 __device__ __forceinline__ void cp_async4(float* dst, const float* src) {
   asm volatile("cp.async.ca.shared.global [%0], [%1], 4;" ::"r"(smem_u32(dst)), "l"(src) : "memory");
@@ -564,39 +578,48 @@ __global__ void __launch_bounds__(kTileThreads, 1)
       }
     } else if (kF8 && warp == kLoaderWarp) {
       // ---------------------------------------------------------- scale loader
-      // Four rows per thread, kScaleKb blocks per slot, asynchronous copies: a row's
-      // scales are contiguous along K, so the copies of a warp touch one 32-byte
-      // sector per row, and run slots ahead of the epilogue.
-      int slot = 0;
-      uint32_t phase = 0;
+      // Four rows per lane, one 16-byte asynchronous copy per row and slot (a row's scales are
+      // contiguous along K), slots ahead of the epilogue.  Single 4-byte copies, a line
+      // each, kept the load path busy for a third of the kernel's time; they remain for scales
+      // that do not start on 16 bytes.
+      const bool vec = (reinterpret_cast<uintptr_t>(args.xs) & 15) == 0;
+      const int64_t total = static_cast<int64_t>(args.n) * nkb;
+      uint32_t slots = 0;  // slots filled so far: slot slots % kScaleSlots is next
       bool ok = true;
       for (int64_t t = unit0; ok && t < num_units; t += stride) {
         const Unit u = find_unit(args, sm->cum, t, num_n, C::kBM, kBN);
-        const float* x[4];
+        int64_t x[4];  // first aligned scale of the lane's rows
 #pragma unroll
         for (int r = 0; r < 4; ++r)
-          x[r] = args.xs +
-                 static_cast<int64_t>(min(u.m0 + static_cast<int>(rank) * kRowTile + lane + 32 * r, u.r1 - 1)) * nkb;
-        // threads 0 .. 7 also bring the weight's scales: block lane / 2 of half lane % 2
+          x[r] = (static_cast<int64_t>(min(u.m0 + static_cast<int>(rank) * kRowTile + lane + 32 * r, u.r1 - 1)) * nkb +
+                  k_begin) & ~int64_t(3);
+        // lanes 0 .. 7 also bring the weight's scales: block lane / 2 of half lane % 2
         const int nb = min((u.n0 + (lane & 1) * (kBN / 2)) >> 7, args.out_blocks - 1);
         const float* w = args.ws + (static_cast<int64_t>(u.e) * args.out_blocks + nb) * nkb;
-        for (int kb0 = k_begin; kb0 < k_end; kb0 += kScaleKb) {
-          if (!wait_bar(smem_u32(&sm->sempty[slot]), phase ^ 1, abort_flag, args.status, args.timeout_ns)) {
+        const int fills = scale_slots(k_end - k_begin);
+        for (int j = 0; j < fills; ++j, ++slots) {
+          const int slot = slots % kScaleSlots;
+          if (!wait_bar(smem_u32(&sm->sempty[slot]), (slots / kScaleSlots & 1) ^ 1, abort_flag, args.status,
+                        args.timeout_ns)) {
             ok = false;
             break;
           }
 #pragma unroll
-          for (int i = 0; i < kScaleKb; ++i) {
-            const int kb = min(kb0 + i, nkb - 1);
+          for (int r = 0; r < 4; ++r) {
+            const int64_t left = total - (x[r] + 4 * j);  // scales from here to the tensor's end
+            float* dst = sm->xs[slot][lane + 32 * r];
+            const float* src = args.xs + (left > 0 ? x[r] + 4 * j : 0);
+            if (vec) {
+              cp_async16(dst, src, left >= 4 ? 16 : left > 0 ? static_cast<int>(left) * 4 : 0);
+            } else {
 #pragma unroll
-            for (int r = 0; r < 4; ++r) cp_async4(&sm->xs[slot][i][lane + 32 * r], x[r] + kb);
+              for (int i = 0; i < 4; ++i)
+                if (i < left) cp_async4(dst + i, src + i);
+            }
           }
-          if (lane < 2 * kScaleKb) cp_async4(&sm->ws[slot][lane >> 1][lane & 1], w + min(kb0 + (lane >> 1), nkb - 1));
+          if (lane < 2 * kScaleKb)
+            cp_async4(&sm->ws[slot][lane >> 1][lane & 1], w + min(k_begin + 4 * j + (lane >> 1), nkb - 1));
           cp_async_arrive(&sm->sfull[slot]);
-          if (++slot == kScaleSlots) {
-            slot = 0;
-            phase ^= 1;
-          }
         }
       }
       asm volatile("cp.async.wait_all;" ::: "memory");
@@ -623,8 +646,9 @@ __global__ void __launch_bounds__(kTileThreads, 1)
       __syncwarp();
       if (lane == 0) mbar_arrive_remote(my_tempty + 8 * C::kHalves * buf);
     };
-    int acc_buf = 0, slot = 0;
-    uint32_t acc_phase = 0, slot_phase = 0;
+    int acc_buf = 0;
+    uint32_t acc_phase = 0;
+    uint32_t slots = 0;  // slots of the scale ring that earlier units took
     bool ok = true;
     for (int64_t t = unit0; ok && t < num_units; t += stride) {
       const Unit u = find_unit(args, sm->cum, t, num_n, C::kBM, kBN);
@@ -634,41 +658,40 @@ __global__ void __launch_bounds__(kTileThreads, 1)
         float acc[kNC];
 #pragma unroll
         for (int i = 0; i < kNC; ++i) acc[i] = 0.f;
+        // The row's scales start `skew` into its 16-byte pieces: block k is in slot (skew + k) / 4.
+        const int blocks = k_end - k_begin;
+        const int skew =
+            (static_cast<uint32_t>(min(row0 + lane, u.r1 - 1)) * static_cast<uint32_t>(nkb) + k_begin) % kScaleKb;
 #pragma unroll 1
-        for (int kb = k_begin; kb < k_end; ++kb) {
-          const int i = (kb - k_begin) % kScaleKb;
-          if (i == 0) {
-            if (!wait_bar(smem_u32(&sm->sfull[slot]), slot_phase, abort_flag, args.status, args.timeout_ns)) {
+        for (int k = 0; k < blocks; ++k) {
+          if (k == 0 || k % kScaleKb == 1) {  // slot (k + 3) / 4 is new to the rows that are furthest ahead
+            const uint32_t j = slots + (k + kScaleKb - 1) / kScaleKb;
+            if (!wait_bar(smem_u32(&sm->sfull[j % kScaleSlots]), j / kScaleSlots & 1, abort_flag, args.status,
+                          args.timeout_ns)) {
               ok = false;
               break;
             }
           }
-          const float s = __fmul_rn(sm->xs[slot][i][quarter * 32 + lane], sm->ws[slot][i][half]);
-          if (i == kScaleKb - 1 || kb == k_end - 1) {
+          const float s = __fmul_rn(
+              sm->xs[(slots + (skew + k) / kScaleKb) % kScaleSlots][quarter * 32 + lane][(skew + k) % kScaleKb],
+              sm->ws[(slots + k / kScaleKb) % kScaleSlots][k % kScaleKb][half]);
+          if (k % kScaleKb == kScaleKb - 1) {  // no row needs slot k / 4 any more
             __syncwarp();
-            if (lane == 0) mbar_arrive(&sm->sempty[slot]);
-            if (++slot == kScaleSlots) {
-              slot = 0;
-              slot_phase ^= 1;
-            }
+            if (lane == 0) mbar_arrive(&sm->sempty[(slots + k / kScaleKb) % kScaleSlots]);
           }
           if (!wait_bar(my_tfull + 8 * C::kHalves * acc_buf, acc_phase, abort_flag, args.status, args.timeout_ns)) {
             ok = false;
             break;
           }
           tc_fence_after();
-          // 32 columns are in flight while the 32 before them are added.
-          uint32_t r[2][32];
-          tmem_ld_32cols(t_lane + acc_buf * kBN, r[0]);
 #pragma unroll
           for (int g = 0; g < kNC / 32; ++g) {
+            uint32_t r[32];
+            tmem_ld_32cols(t_lane + acc_buf * kBN + g * 32, r);
             tmem_ld_wait();
-            if (g + 1 < kNC / 32)
-              tmem_ld_32cols(t_lane + acc_buf * kBN + (g + 1) * 32, r[(g + 1) & 1]);
-            else
-              release(acc_buf);
+            if (g == kNC / 32 - 1) release(acc_buf);
 #pragma unroll
-            for (int j = 0; j < 32; ++j) acc[g * 32 + j] = fmaf(__uint_as_float(r[g & 1][j]), s, acc[g * 32 + j]);
+            for (int j = 0; j < 32; ++j) acc[g * 32 + j] = fmaf(__uint_as_float(r[j]), s, acc[g * 32 + j]);
           }
           if (++acc_buf == C::kAccs) {
             acc_buf = 0;
@@ -676,6 +699,11 @@ __global__ void __launch_bounds__(kTileThreads, 1)
           }
         }
         if (!ok) break;
+        __syncwarp();
+        if (lane == 0)
+          for (int j = blocks / kScaleKb; j < scale_slots(blocks); ++j)
+            mbar_arrive(&sm->sempty[(slots + j) % kScaleSlots]);
+        slots += scale_slots(blocks);
         if (split) {
           // This share's sums, for the exchange below: [column / 4][row], 16 bytes each.
           float4* part = reinterpret_cast<float4*>(smem) + half * (kNC / 4) * kRowTile + quarter * 32 + lane;
@@ -730,7 +758,7 @@ __global__ void __launch_bounds__(kTileThreads, 1)
         }
       }
     }
-    asm volatile("cp.async.bulk.wait_group 0;" ::: "memory");
+    asm volatile("cp.async.bulk.wait_group.read 0;" ::: "memory");
     if (split) {
       // Every CTA of the cluster adds its columns of the tile over the shares, in order.
       // (The operand stages are free: the accumulator's last hand-over follows every MMA.)
@@ -772,21 +800,23 @@ __global__ void __launch_bounds__(kTileThreads, 1)
 }
 
 // ---------------------------------------------------------------------------
-// Skinny kernel: 16 rows of W per CTA, the K blocks dealt to its 8 warps.
+// Skinny kernel: 16 kMR rows of W per CTA, the K blocks dealt to its 8 warps.
 //
 // A K block (128 bytes) of a warp is two 64-byte pieces; lane (g, q) holds bytes
-// 16 q .. 16 q + 15 of each piece for weight rows g and g + 8 and for row g of each
-// 8-row tile of X.  The m16n8 instructions take, from lane (g, q), two 4-byte
-// registers per operand row; which columns of K they stand for does not matter as
-// long as W and X agree, so the four registers of a 16-byte load feed two
-// instructions as they are.
+// 16 q .. 16 q + 15 of each piece for weight rows g and g + 8 of each 16-row tile and for
+// row g of each 8-row tile of X.  The m16n8k16 instructions take, from lane (g, q), two
+// 4-byte registers (pairs of 16-bit values) per operand row; which columns of K they stand
+// for does not matter as long as W and X agree.  So bf16 registers feed them as they are,
+// and a register of four e4m3 values becomes the two halves of an fp16 operand (exact:
+// e4m3 is a subset of fp16).  The e4m3 form of the instruction does the same conversion
+// for every product anew; converting each operand once is what makes several tiles cheap.
 // ---------------------------------------------------------------------------
 
 template <bool kF8>
 __device__ __forceinline__ void mma_16x8(float (&c)[4], uint32_t a0, uint32_t a1, uint32_t a2, uint32_t a3, uint32_t b0,
                                          uint32_t b1) {
   if (kF8)
-    asm("mma.sync.aligned.m16n8k32.row.col.f32.e4m3.e4m3.f32 {%0, %1, %2, %3}, {%4, %5, %6, %7}, {%8, %9}, "
+    asm("mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0, %1, %2, %3}, {%4, %5, %6, %7}, {%8, %9}, "
         "{%0, %1, %2, %3};"
         : "+f"(c[0]), "+f"(c[1]), "+f"(c[2]), "+f"(c[3])
         : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1));
@@ -797,37 +827,64 @@ __device__ __forceinline__ void mma_16x8(float (&c)[4], uint32_t a0, uint32_t a1
         : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1));
 }
 
-constexpr int kSkinnyWarps = 8;
-constexpr int kSkinnyRows = 16;
+// Four e4m3 values as two fp16 pairs (exact; NaN stays NaN).
+__device__ __forceinline__ void e4m3_to_f16(uint32_t v, uint32_t& lo, uint32_t& hi) {
+  asm("{\n\t.reg .b16 l, h;\n\tmov.b32 {l, h}, %2;\n\t"
+      "cvt.rn.f16x2.e4m3x2 %0, l;\n\tcvt.rn.f16x2.e4m3x2 %1, h;\n\t}"
+      : "=r"(lo), "=r"(hi)
+      : "r"(v));
+}
 
-template <bool kF8, int kNT>  // kNT tiles of 8 rows of X per pass
+// A 16-byte piece as the operand registers of the instructions it feeds: 8 of fp16 pairs (4 k16
+// steps of two), or the 4 it has (2 steps of two).
+template <bool kF8>
+struct Piece {
+  static constexpr int kSteps = kF8 ? 4 : 2;
+  uint32_t r[kSteps][2];
+  __device__ __forceinline__ explicit Piece(const uint4& v) {
+    if constexpr (kF8) {
+      e4m3_to_f16(v.x, r[0][0], r[0][1]);
+      e4m3_to_f16(v.y, r[1][0], r[1][1]);
+      e4m3_to_f16(v.z, r[2][0], r[2][1]);
+      e4m3_to_f16(v.w, r[3][0], r[3][1]);
+    } else {
+      r[0][0] = v.x, r[0][1] = v.y, r[1][0] = v.z, r[1][1] = v.w;
+    }
+  }
+};
+
+constexpr int kSkinnyWarps = 8;
+
+template <bool kF8, int kNT, int kMR, int kU>  // kNT tiles of 8 rows of X per pass, kU K blocks in flight per warp
 __global__ void __launch_bounds__(32 * kSkinnyWarps) skinny_kernel(const __grid_constant__ ProductArgs a) {
-  constexpr int kU = 2;           // K blocks in flight per warp
   constexpr int kTok = 8 * kNT;
-  __shared__ float red[kSkinnyWarps][kTok][kSkinnyRows + 1];
+  constexpr int kRows = 16 * kMR;
+  __shared__ float red[kSkinnyWarps][kTok][kRows + 1];
   const int e = blockIdx.y;
   int r0, r1;
   expert_rows(a, e, r0, r1);
   if (r0 >= r1) return;
-  const int o0 = blockIdx.x * kSkinnyRows;
+  const int o0 = blockIdx.x * kRows;
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   const int g = lane >> 2, q = lane & 3;
   const int in_bytes = a.in * (kF8 ? 1 : 2);  // a multiple of 16
-  const bool w_ok[2] = {o0 + g < a.out, o0 + g + 8 < a.out};
   const int64_t w_off = (static_cast<int64_t>(e) * a.out + o0 + g) * a.ldw + q * 16;
+  // (the rows of a CTA lie in one 128-row scale block: kRows divides 128)
   const float* ws = kF8 ? a.ws + (static_cast<int64_t>(e) * a.out_blocks + (o0 >> 7)) * a.nkb : nullptr;
   const int segs = (!kF8 && a.W_lo) ? 2 : 1;
 
   for (int t0 = r0; t0 < r1; t0 += kTok) {
-    float acc[kNT][4];
+    float acc[kMR][kNT][4];
 #pragma unroll
-    for (int nt = 0; nt < kNT; ++nt)
+    for (int m = 0; m < kMR; ++m)
 #pragma unroll
-      for (int i = 0; i < 4; ++i) acc[nt][i] = 0.f;
+      for (int nt = 0; nt < kNT; ++nt)
+#pragma unroll
+        for (int i = 0; i < 4; ++i) acc[m][nt][i] = 0.f;
     for (int seg = 0; seg < segs; ++seg) {
       const uint8_t* wp = static_cast<const uint8_t*>(seg ? a.W_lo : a.W) + w_off;
       for (int kb0 = warp; kb0 < a.nkb; kb0 += kU * kSkinnyWarps) {
-        uint4 w[kU][2][2], x[kU][2][kNT];
+        uint4 w[kU][kMR][2][2], x[kU][kNT][2];
         float sx[kU][kNT][2], sw[kU];
 #pragma unroll
         for (int j = 0; j < kU; ++j) {
@@ -837,21 +894,24 @@ __global__ void __launch_bounds__(32 * kSkinnyWarps) skinny_kernel(const __grid_
             const int k = kb * kKBytes + c * 64;
             const bool k_ok = k + q * 16 < in_bytes;  // also false for kb past the end
 #pragma unroll
-            for (int h = 0; h < 2; ++h) {
-              w[j][c][h] = make_uint4(0, 0, 0, 0);
-              if (k_ok && w_ok[h]) {
-                const uint8_t* p = wp + h * 8 * a.ldw + k;
-                asm("ld.global.nc.L1::no_allocate.v4.u32 {%0, %1, %2, %3}, [%4];"
-                    : "=r"(w[j][c][h].x), "=r"(w[j][c][h].y), "=r"(w[j][c][h].z), "=r"(w[j][c][h].w)
-                    : "l"(p));
+            for (int m = 0; m < kMR; ++m)
+#pragma unroll
+              for (int h = 0; h < 2; ++h) {
+                uint4& v = w[j][m][c][h];
+                v = make_uint4(0, 0, 0, 0);
+                if (k_ok && o0 + m * 16 + h * 8 + g < a.out) {
+                  const uint8_t* p = wp + static_cast<int64_t>(m * 16 + h * 8) * a.ldw + k;
+                  asm("ld.global.nc.L1::no_allocate.v4.u32 {%0, %1, %2, %3}, [%4];"
+                      : "=r"(v.x), "=r"(v.y), "=r"(v.z), "=r"(v.w)
+                      : "l"(p));
+                }
               }
-            }
 #pragma unroll
             for (int nt = 0; nt < kNT; ++nt) {
-              x[j][c][nt] = make_uint4(0, 0, 0, 0);
+              x[j][nt][c] = make_uint4(0, 0, 0, 0);
               const int row = t0 + nt * 8 + g;
               if (k_ok && row < r1)
-                x[j][c][nt] = __ldg(reinterpret_cast<const uint4*>(static_cast<const uint8_t*>(a.X) +
+                x[j][nt][c] = __ldg(reinterpret_cast<const uint4*>(static_cast<const uint8_t*>(a.X) +
                                                                    static_cast<int64_t>(row) * a.ldx + q * 16 + k));
             }
           }
@@ -869,22 +929,42 @@ __global__ void __launch_bounds__(32 * kSkinnyWarps) skinny_kernel(const __grid_
         }
 #pragma unroll
         for (int j = 0; j < kU; ++j) {
+          if (j > 0 && kb0 + j * kSkinnyWarps >= a.nkb) break;  // (a block past the end has no scales)
+          float part[kMR][kNT][4];
+          if (kF8) {
 #pragma unroll
-          for (int nt = 0; nt < kNT; ++nt) {
-            float part[4] = {0.f, 0.f, 0.f, 0.f};
-            float(&c4)[4] = kF8 ? part : acc[nt];
+            for (int m = 0; m < kMR; ++m)
 #pragma unroll
-            for (int c = 0; c < 2; ++c) {
-              const uint4 lo = w[j][c][0], hi = w[j][c][1], xx = x[j][c][nt];
-              mma_16x8<kF8>(c4, lo.x, hi.x, lo.y, hi.y, xx.x, xx.y);
-              mma_16x8<kF8>(c4, lo.z, hi.z, lo.w, hi.w, xx.z, xx.w);
+              for (int nt = 0; nt < kNT; ++nt)
+#pragma unroll
+                for (int i = 0; i < 4; ++i) part[m][nt][i] = 0.f;
+          }
+#pragma unroll
+          for (int c = 0; c < 2; ++c) {
+#pragma unroll
+            for (int m = 0; m < kMR; ++m) {
+              const Piece<kF8> lo(w[j][m][c][0]), hi(w[j][m][c][1]);
+#pragma unroll
+              for (int nt = 0; nt < kNT; ++nt) {
+                const Piece<kF8> xx(x[j][nt][c]);
+#pragma unroll
+                for (int s = 0; s < Piece<kF8>::kSteps; ++s)
+                  mma_16x8<kF8>(kF8 ? part[m][nt] : acc[m][nt], lo.r[s][0], hi.r[s][0], lo.r[s][1], hi.r[s][1],
+                                xx.r[s][0], xx.r[s][1]);
+              }
             }
-            if (kF8 && kb0 + j * kSkinnyWarps < a.nkb) {
+          }
+          if (kF8) {
+#pragma unroll
+            for (int nt = 0; nt < kNT; ++nt) {
               const float s0 = __fmul_rn(sx[j][nt][0], sw[j]), s1 = __fmul_rn(sx[j][nt][1], sw[j]);
-              acc[nt][0] = fmaf(part[0], s0, acc[nt][0]);
-              acc[nt][1] = fmaf(part[1], s1, acc[nt][1]);
-              acc[nt][2] = fmaf(part[2], s0, acc[nt][2]);
-              acc[nt][3] = fmaf(part[3], s1, acc[nt][3]);
+#pragma unroll
+              for (int m = 0; m < kMR; ++m) {
+                acc[m][nt][0] = fmaf(part[m][nt][0], s0, acc[m][nt][0]);
+                acc[m][nt][1] = fmaf(part[m][nt][1], s1, acc[m][nt][1]);
+                acc[m][nt][2] = fmaf(part[m][nt][2], s0, acc[m][nt][2]);
+                acc[m][nt][3] = fmaf(part[m][nt][3], s1, acc[m][nt][3]);
+              }
             }
           }
         }
@@ -892,15 +972,17 @@ __global__ void __launch_bounds__(32 * kSkinnyWarps) skinny_kernel(const __grid_
     }
     // c0, c1: weight row g, rows 2q and 2q + 1 of X; c2, c3: weight row g + 8.
 #pragma unroll
-    for (int nt = 0; nt < kNT; ++nt) {
-      red[warp][nt * 8 + q * 2][g] = acc[nt][0];
-      red[warp][nt * 8 + q * 2 + 1][g] = acc[nt][1];
-      red[warp][nt * 8 + q * 2][g + 8] = acc[nt][2];
-      red[warp][nt * 8 + q * 2 + 1][g + 8] = acc[nt][3];
-    }
+    for (int m = 0; m < kMR; ++m)
+#pragma unroll
+      for (int nt = 0; nt < kNT; ++nt) {
+        red[warp][nt * 8 + q * 2][m * 16 + g] = acc[m][nt][0];
+        red[warp][nt * 8 + q * 2 + 1][m * 16 + g] = acc[m][nt][1];
+        red[warp][nt * 8 + q * 2][m * 16 + g + 8] = acc[m][nt][2];
+        red[warp][nt * 8 + q * 2 + 1][m * 16 + g + 8] = acc[m][nt][3];
+      }
     __syncthreads();
-    for (int i = threadIdx.x; i < kTok * kSkinnyRows; i += 32 * kSkinnyWarps) {
-      const int o = i % kSkinnyRows, tok = i / kSkinnyRows;
+    for (int i = threadIdx.x; i < kTok * kRows; i += 32 * kSkinnyWarps) {
+      const int o = i % kRows, tok = i / kRows;
       if (t0 + tok < r1 && o0 + o < a.out) {
         float v = 0.f;
 #pragma unroll
@@ -911,6 +993,13 @@ __global__ void __launch_bounds__(32 * kSkinnyWarps) skinny_kernel(const __grid_
     }
     __syncthreads();
   }
+}
+
+template <bool kF8, int kNT, int kMR, int kU>
+cudaError_t launch_skinny(const ProductArgs& a, cudaStream_t st) {
+  const dim3 grid((a.out + 16 * kMR - 1) / (16 * kMR), a.experts);
+  skinny_kernel<kF8, kNT, kMR, kU><<<grid, 32 * kSkinnyWarps, 0, st>>>(a);
+  return cudaGetLastError();
 }
 
 // ---------------------------------------------------------------------------
@@ -998,17 +1087,20 @@ cudaError_t launch_tile(ProductArgs a, const DeviceInfo& d, cudaStream_t st, int
 
 template <bool kF8>
 cudaError_t launch_type(const ProductArgs& a, const DeviceInfo& d, cudaStream_t st) {
-  const int64_t per = (static_cast<int64_t>(a.n) + a.experts - 1) / a.experts;  // rows per expert, on average
-  if (per <= 32) {
-    const dim3 grid((a.out + kSkinnyRows - 1) / kSkinnyRows, a.experts);
-    if (per <= 8)
-      skinny_kernel<kF8, 1><<<grid, 32 * kSkinnyWarps, 0, st>>>(a);
-    else if (per <= 16)
-      skinny_kernel<kF8, 2><<<grid, 32 * kSkinnyWarps, 0, st>>>(a);
-    else
-      skinny_kernel<kF8, 4><<<grid, 32 * kSkinnyWarps, 0, st>>>(a);
-    return cudaGetLastError();
+  if (const char* f = getenv("AR_FORCE")) {  // XXX
+#define SK(NAME, NT, MR, U) if (!strcmp(f, NAME)) return launch_skinny<kF8, NT, MR, U>(a, st)
+    SK("s1.1.2", 1, 1, 2); SK("s1.1.1", 1, 1, 1); SK("s1.2.2", 1, 2, 2); SK("s1.2.1", 1, 2, 1);
+    SK("s2.2.1", 2, 2, 1); SK("s2.1.1", 2, 1, 1);
+    SK("s4.2.1", 4, 2, 1); SK("s4.1.1", 4, 1, 1);
+#undef SK
+    if (!strcmp(f, "p")) return launch_tile<kF8, true, 256>(a, d, st);
+    if (!strcmp(f, "w")) return launch_tile<kF8, false, 256>(a, d, st);
+    if (f[0] == 't') return launch_tile<kF8, false, 128>(a, d, st, atoi(f + 1));
   }
+  const int64_t per = (static_cast<int64_t>(a.n) + a.experts - 1) / a.experts;  // rows per expert, on average
+  if (per <= 8) return launch_skinny<kF8, 1, 1, 2>(a, st);
+  if (per <= 16) return launch_skinny<kF8, 2, 1, 2>(a, st);
+  if (per <= 32) return launch_skinny<kF8, 4, 1, 2>(a, st);
   const char* ev = getenv("AR_TILE");
   const int tv = ev ? atoi(ev) : 0;
   if (tv == 2) return launch_tile<kF8, true, 256>(a, d, st);
