@@ -16,8 +16,6 @@
 //   * skinny_kernel: few rows per expert, bound by the weight's bytes; each weight
 //     byte goes from HBM straight into the registers of the warp that multiplies it.
 #include <stddef.h>
-#include <stdlib.h>
-#include <string.h>
 
 #include <atomic>
 
@@ -588,11 +586,12 @@ __global__ void __launch_bounds__(kTileThreads, 1)
       bool ok = true;
       for (int64_t t = unit0; ok && t < num_units; t += stride) {
         const Unit u = find_unit(args, sm->cum, t, num_n, C::kBM, kBN);
-        int64_t x[4];  // first aligned scale of the lane's rows
+        int64_t x[4];  // first aligned scale of the lane's rows; rows past the expert's end: past the tensor's
 #pragma unroll
-        for (int r = 0; r < 4; ++r)
-          x[r] = (static_cast<int64_t>(min(u.m0 + static_cast<int>(rank) * kRowTile + lane + 32 * r, u.r1 - 1)) * nkb +
-                  k_begin) & ~int64_t(3);
+        for (int r = 0; r < 4; ++r) {
+          const int row = u.m0 + static_cast<int>(rank) * kRowTile + lane + 32 * r;
+          x[r] = row < u.r1 ? (static_cast<int64_t>(row) * nkb + k_begin) & ~int64_t(3) : total;
+        }
         // lanes 0 .. 7 also bring the weight's scales: block lane / 2 of half lane % 2
         const int nb = min((u.n0 + (lane & 1) * (kBN / 2)) >> 7, args.out_blocks - 1);
         const float* w = args.ws + (static_cast<int64_t>(u.e) * args.out_blocks + nb) * nkb;
@@ -661,7 +660,7 @@ __global__ void __launch_bounds__(kTileThreads, 1)
         // The row's scales start `skew` into its 16-byte pieces: block k is in slot (skew + k) / 4.
         const int blocks = k_end - k_begin;
         const int skew =
-            (static_cast<uint32_t>(min(row0 + lane, u.r1 - 1)) * static_cast<uint32_t>(nkb) + k_begin) % kScaleKb;
+            (static_cast<uint32_t>(row0 + lane) * static_cast<uint32_t>(nkb) + k_begin) % kScaleKb;
 #pragma unroll 1
         for (int k = 0; k < blocks; ++k) {
           if (k == 0 || k % kScaleKb == 1) {  // slot (k + 3) / 4 is new to the rows that are furthest ahead
@@ -1085,28 +1084,55 @@ cudaError_t launch_tile(ProductArgs a, const DeviceInfo& d, cudaStream_t st, int
   return cudaLaunchKernelEx(&cfg, fn, mx, mw, mlo, a);
 }
 
+// Which kernel.  Both operand types, times on one B200 in us.
+//
+// Rows per expert (on average) decide between the two kernels.  The skinny one has no
+// fixed cost but walks W again for every kTok rows; the tile one starts at 8 us (tensor
+// memory, barriers, descriptors, the first loads) and then takes 128 rows for the price of one.
+//   n = 1,  4096 -> 4096:  skinny 6.5, tile 12        n = 32, 4096 -> 4096:  skinny 10.9, tile 12.4
+//   n = 16, 29568 -> 8192: skinny 56, tile 63         n = 32, 29568 -> 8192: skinny 104, tile 62
+//   64 experts, 2048 -> 1024, 4 rows each: 30 and 38; 8 rows: 38 and 38; 16 rows: 50 and 39
+// Several experts are taken to be uneven (some have several times the average).
+//
+// Among the tiles, 128 x 128 on one SM, 128 x 256 on one SM and 256 x 256 on a pair, the
+// fewest waves times the cost of a wave: e4m3, K = 4096: 16, 26.5 and 25 us a wave (n = 16384,
+// 4096 -> 11008: 1157, 1022, 933 in all; n = 333: 35, 28, 56; n = 512, 4096 -> 4096: 19, 26, 25);
+// bf16: 13, 21 and 20 for 2048 columns of K.  With half the SMs idle or more, 128 x 128
+// tiles share their K blocks among a cluster of 2 or 4 CTAs (n = 64, 4096 -> 4096: 19 alone,
+// 16 and 12.8 shared; 29568 -> 8192: 104, 61).  A cluster of 8 gained nothing more (7.6 for
+// 7.7 at 1024 -> 1000) and lost up to twice the time.
 template <bool kF8>
 cudaError_t launch_type(const ProductArgs& a, const DeviceInfo& d, cudaStream_t st) {
-  if (const char* f = getenv("AR_FORCE")) {  // XXX
-#define SK(NAME, NT, MR, U) if (!strcmp(f, NAME)) return launch_skinny<kF8, NT, MR, U>(a, st)
-    SK("s1.1.2", 1, 1, 2); SK("s1.1.1", 1, 1, 1); SK("s1.2.2", 1, 2, 2); SK("s1.2.1", 1, 2, 1);
-    SK("s2.2.1", 2, 2, 1); SK("s2.1.1", 2, 1, 1);
-    SK("s4.2.1", 4, 2, 1); SK("s4.1.1", 4, 1, 1);
-#undef SK
-    if (!strcmp(f, "p")) return launch_tile<kF8, true, 256>(a, d, st);
-    if (!strcmp(f, "w")) return launch_tile<kF8, false, 256>(a, d, st);
-    if (f[0] == 't') return launch_tile<kF8, false, 128>(a, d, st, atoi(f + 1));
+  const int64_t per = (static_cast<int64_t>(a.n) + a.experts - 1) / a.experts;
+  const int64_t strips = (a.out + 15) / 16;  // 16-row strips of one W
+  if (per <= 8) {
+    // Two strips per CTA halve the conversions of X, where enough CTAs are left (e4m3 only:
+    // 29568 -> 8192 56 -> 50; bf16 operands need none).
+    if (kF8 && strips / 2 * a.experts >= d.sms * 3 / 2) return launch_skinny<kF8, 1, 2, 1>(a, st);
+    return launch_skinny<kF8, 1, 1, 2>(a, st);
   }
-  const int64_t per = (static_cast<int64_t>(a.n) + a.experts - 1) / a.experts;  // rows per expert, on average
-  if (per <= 8) return launch_skinny<kF8, 1, 1, 2>(a, st);
-  if (per <= 16) return launch_skinny<kF8, 2, 1, 2>(a, st);
-  if (per <= 32) return launch_skinny<kF8, 4, 1, 2>(a, st);
-  const char* ev = getenv("AR_TILE");
-  const int tv = ev ? atoi(ev) : 0;
-  if (tv == 2) return launch_tile<kF8, true, 256>(a, d, st);
-  if (tv == 1) return launch_tile<kF8, false, 256>(a, d, st);
-  const char* es = getenv("AR_SPLIT");
-  return launch_tile<kF8, false, 128>(a, d, st, es ? atoi(es) : 1);
+  if (a.experts == 1) {
+    if (per <= 16) return launch_skinny<kF8, 2, 2, 1>(a, st);
+    if (per <= 64 && (per + 31) / 32 * strips * a.nkb <= 8192) return launch_skinny<kF8, 4, 1, 1>(a, st);
+  }
+  // Row blocks: exact for one expert, else half a block more per expert, and one at least.
+  const int64_t active = a.experts < a.n ? a.experts : a.n;
+  auto waves = [&](int bm, int bn, int resident) {
+    const int64_t cols = (a.out + bn - 1) / bn;
+    if (a.experts == 1) return static_cast<double>(((a.n + bm - 1) / bm * cols + resident - 1) / resident);
+    const double rows = static_cast<double>(a.n) / bm + 0.5 * active;
+    const double units = (rows > active ? rows : active) * cols;
+    return units > resident ? units / resident : 1.0;
+  };
+  const double small = waves(128, 128, d.sms) * (kF8 ? 16.0 : 13.0);
+  const double wide = waves(128, 256, d.sms) * (kF8 ? 26.5 : 21.0);
+  const double pair = waves(256, 256, d.sms / 2) * (kF8 ? 25.0 : 20.0);
+  if (small <= wide && small <= pair) {
+    const int64_t units = units_at_most(a, 128, 128);
+    return launch_tile<kF8, false, 128>(a, d, st, units * 4 <= d.sms ? 4 : units * 2 <= d.sms ? 2 : 1);
+  }
+  if (wide <= pair) return launch_tile<kF8, false, 256>(a, d, st);
+  return launch_tile<kF8, true, 256>(a, d, st);
 }
 
 }  // namespace
