@@ -21,6 +21,7 @@ struct RmsNormArgs {
   const void* weight = nullptr;     // [cols]; null: ones
   int w_bf16 = 1;
   float eps = 0.f;
+  float inv_cols = 0.f;             // 1 / cols (set by the launch)
   void* sum = nullptr;              // the residual's type; may be the residual itself
   int64_t lds = 0;
   uint16_t* y = nullptr;

@@ -26,17 +26,24 @@ constexpr float kE4m3Max = 448.0f;
 struct Bf16Oct {
   uint4 v;
 };
+struct Bf16Raw {  // loaded one by one: packing them would wait for the loads
+  uint16_t e[8];
+};
 struct F32Oct {
   float4 a, b;
 };
 
-template <bool kBf16>
+template <bool kBf16, bool kVec>
 struct OctOf {
   using type = F32Oct;
 };
 template <>
-struct OctOf<true> {
+struct OctOf<true, true> {
   using type = Bf16Oct;
+};
+template <>
+struct OctOf<true, false> {
+  using type = Bf16Raw;
 };
 
 __device__ __forceinline__ uint4 ldg_stream(const void* p) {
@@ -47,45 +54,55 @@ __device__ __forceinline__ uint4 ldg_stream(const void* p) {
   return v;
 }
 
-// Columns [col, col + 8) of the row at element offset `row0`; those at or past
-// `cols` read as 0.  kVec: 16-byte loads (the caller checked alignment and that
-// cols is a multiple of 8).  The plain ld (not .nc) is for inputs that may be the
-// buffer the same kernel writes (kAlias).
+// Eight elements of a lane: where they are.  With 16-byte accesses (kVec: aligned rows,
+// cols a multiple of 8) they are eight consecutive columns.  Without, element k is column
+// col + 32 (k % 4) of one of two 128-column blocks (k < 4, k >= 4), so that a load or store
+// instruction of the warp covers consecutive elements: eight consecutive columns per lane
+// would touch 16 sectors per instruction instead of 2, and ran four times longer.
+struct Place {
+  int64_t row0, row1;  // element offsets of the rows of k < 4 and k >= 4 (kVec: row0)
+  int col0, col1;      // first column (kVec: of all eight; else of the lane)
+};
+
+__device__ __forceinline__ int place_col(const Place& p, int k) { return (k < 4 ? p.col0 : p.col1) + 32 * (k & 3); }
+__device__ __forceinline__ int64_t place_at(const Place& p, int k) { return (k < 4 ? p.row0 : p.row1) + place_col(p, k); }
+
+// Elements at or past `cols` read as 0.  The plain ld (not .nc) is for inputs that may be
+// the buffer the same kernel writes (kAlias).
 template <bool kVec, bool kAlias = false>
-__device__ __forceinline__ Bf16Oct load_oct(const uint16_t* p, int64_t row0, int col, int cols) {
-  Bf16Oct o;
-  o.v = make_uint4(0, 0, 0, 0);
-  if (col >= cols) return o;
-  if (kVec) {
-    o.v = kAlias ? *reinterpret_cast<const uint4*>(p + row0 + col) : ldg_stream(p + row0 + col);
+__device__ __forceinline__ typename OctOf<true, kVec>::type load_oct(const uint16_t* p, const Place& at, int cols) {
+  typename OctOf<true, kVec>::type o;
+  if constexpr (kVec) {
+    o.v = make_uint4(0, 0, 0, 0);
+    if (at.col0 < cols)
+      o.v = kAlias ? *reinterpret_cast<const uint4*>(p + at.row0 + at.col0) : ldg_stream(p + at.row0 + at.col0);
   } else {
-    uint32_t e[8];
 #pragma unroll
-    for (int i = 0; i < 8; ++i) e[i] = col + i < cols ? p[row0 + col + i] : 0u;
-    o.v = make_uint4(e[0] | (e[1] << 16), e[2] | (e[3] << 16), e[4] | (e[5] << 16), e[6] | (e[7] << 16));
+    for (int k = 0; k < 8; ++k) o.e[k] = place_col(at, k) < cols ? p[place_at(at, k)] : uint16_t(0);
   }
   return o;
 }
 
 template <bool kVec, bool kAlias = false>
-__device__ __forceinline__ F32Oct load_oct(const float* p, int64_t row0, int col, int cols) {
+__device__ __forceinline__ F32Oct load_oct(const float* p, const Place& at, int cols) {
   F32Oct o;
   o.a = make_float4(0.f, 0.f, 0.f, 0.f);
   o.b = o.a;
-  if (col >= cols) return o;
   if (kVec) {
+    if (at.col0 >= cols) return o;
+    const float* q = p + at.row0 + at.col0;
     if (kAlias) {
-      o.a = *reinterpret_cast<const float4*>(p + row0 + col);
-      o.b = *reinterpret_cast<const float4*>(p + row0 + col + 4);
+      o.a = *reinterpret_cast<const float4*>(q);
+      o.b = *reinterpret_cast<const float4*>(q + 4);
     } else {
-      const uint4 x = ldg_stream(p + row0 + col), y = ldg_stream(p + row0 + col + 4);
+      const uint4 x = ldg_stream(q), y = ldg_stream(q + 4);
       o.a = make_float4(__uint_as_float(x.x), __uint_as_float(x.y), __uint_as_float(x.z), __uint_as_float(x.w));
       o.b = make_float4(__uint_as_float(y.x), __uint_as_float(y.y), __uint_as_float(y.z), __uint_as_float(y.w));
     }
   } else {
     float e[8];
 #pragma unroll
-    for (int i = 0; i < 8; ++i) e[i] = col + i < cols ? p[row0 + col + i] : 0.f;
+    for (int k = 0; k < 8; ++k) e[k] = place_col(at, k) < cols ? p[place_at(at, k)] : 0.f;
     o.a = make_float4(e[0], e[1], e[2], e[3]);
     o.b = make_float4(e[4], e[5], e[6], e[7]);
   }
@@ -101,14 +118,18 @@ __device__ __forceinline__ void unpack(const Bf16Oct& o, float (&f)[8]) {
   }
 }
 
+__device__ __forceinline__ void unpack(const Bf16Raw& o, float (&f)[8]) {
+#pragma unroll
+  for (int k = 0; k < 8; ++k) f[k] = bf16_bits_to_f32(o.e[k]);
+}
+
 __device__ __forceinline__ void unpack(const F32Oct& o, float (&f)[8]) {
   f[0] = o.a.x, f[1] = o.a.y, f[2] = o.a.z, f[3] = o.a.w;
   f[4] = o.b.x, f[5] = o.b.y, f[6] = o.b.z, f[7] = o.b.w;
 }
 
 template <bool kVec>
-__device__ __forceinline__ void store_oct(uint16_t* p, int64_t row0, int col, int cols, const float (&f)[8]) {
-  if (col >= cols) return;
+__device__ __forceinline__ void store_oct(uint16_t* p, const Place& at, int cols, const float (&f)[8]) {
   uint32_t w[4];
 #pragma unroll
   for (int i = 0; i < 4; ++i) {
@@ -116,24 +137,25 @@ __device__ __forceinline__ void store_oct(uint16_t* p, int64_t row0, int col, in
     w[i] = *reinterpret_cast<const uint32_t*>(&h);
   }
   if (kVec) {
-    *reinterpret_cast<uint4*>(p + row0 + col) = make_uint4(w[0], w[1], w[2], w[3]);
+    if (at.col0 < cols) *reinterpret_cast<uint4*>(p + at.row0 + at.col0) = make_uint4(w[0], w[1], w[2], w[3]);
   } else {
 #pragma unroll
-    for (int i = 0; i < 8; ++i)
-      if (col + i < cols) p[row0 + col + i] = static_cast<uint16_t>(w[i / 2] >> (16 * (i & 1)));
+    for (int k = 0; k < 8; ++k)
+      if (place_col(at, k) < cols) p[place_at(at, k)] = static_cast<uint16_t>(w[k / 2] >> (16 * (k & 1)));
   }
 }
 
 template <bool kVec>
-__device__ __forceinline__ void store_oct(float* p, int64_t row0, int col, int cols, const float (&f)[8]) {
-  if (col >= cols) return;
+__device__ __forceinline__ void store_oct(float* p, const Place& at, int cols, const float (&f)[8]) {
   if (kVec) {
-    *reinterpret_cast<float4*>(p + row0 + col) = make_float4(f[0], f[1], f[2], f[3]);
-    *reinterpret_cast<float4*>(p + row0 + col + 4) = make_float4(f[4], f[5], f[6], f[7]);
+    if (at.col0 >= cols) return;
+    float* q = p + at.row0 + at.col0;
+    *reinterpret_cast<float4*>(q) = make_float4(f[0], f[1], f[2], f[3]);
+    *reinterpret_cast<float4*>(q + 4) = make_float4(f[4], f[5], f[6], f[7]);
   } else {
 #pragma unroll
-    for (int i = 0; i < 8; ++i)
-      if (col + i < cols) p[row0 + col + i] = f[i];
+    for (int k = 0; k < 8; ++k)
+      if (place_col(at, k) < cols) p[place_at(at, k)] = f[k];
   }
 }
 
@@ -158,23 +180,38 @@ struct BlockScale {
   bool fast;
 };
 
+// The scale and its reciprocal cost as much as the block's quotients if they come from full
+// divisions, so in the fast range they do not either: amax / 448 by div_rn_by with the
+// constant's reciprocal, and 1/s from the hardware's approximation (within one unit) by one
+// Newton step with fma, which gives the correctly rounded reciprocal of every s whose
+// significand is not all ones (Markstein 1990, as div_rn_by); those take the slow path.
 __device__ __forceinline__ BlockScale block_scale(float amax) {
   BlockScale b;
-  b.s = __fdiv_rn(amax, kE4m3Max);
-  if (b.s == 0.0f) b.s = 1.0f;
-  b.rcp = __frcp_rn(b.s);
-  b.fast = b.s >= 0x1p-80f && b.s <= 0x1p100f;
+  b.fast = amax >= 0x1p-70f && amax <= 0x1p100f;
+  b.s = div_rn_by(amax, kE4m3Max, 1.0f / kE4m3Max);
+  b.fast = b.fast && (__float_as_uint(b.s) & 0x7FFFFFu) != 0x7FFFFFu;
+  float y;
+  asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(b.s));
+  b.rcp = __fmaf_rn(__fmaf_rn(-b.s, y, 1.0f), y, y);
+  if (!b.fast) {
+    b.s = __fdiv_rn(amax, kE4m3Max);
+    if (b.s == 0.0f) {
+      b.s = 1.0f;
+      b.rcp = 1.0f;
+      b.fast = amax == 0.0f;  // (past the end of rows, for one: every quotient is 0)
+    }
+  }
   return b;
 }
 
-__device__ __forceinline__ uint2 quant_oct(const float (&f)[8], const BlockScale& b) {
+__device__ __forceinline__ uint2 quant_oct(const float (&f)[8], const BlockScale& b0, const BlockScale& b1) {
   float u[8];
-  if (b.fast) {
+  if (b0.fast && b1.fast) {
 #pragma unroll
-    for (int i = 0; i < 8; ++i) u[i] = div_rn_by(f[i], b.s, b.rcp);
+    for (int i = 0; i < 8; ++i) u[i] = div_rn_by(f[i], (i < 4 ? b0 : b1).s, (i < 4 ? b0 : b1).rcp);
   } else {
 #pragma unroll
-    for (int i = 0; i < 8; ++i) u[i] = __fdiv_rn(f[i], b.s);
+    for (int i = 0; i < 8; ++i) u[i] = __fdiv_rn(f[i], (i < 4 ? b0 : b1).s);
   }
   uint32_t w[2];
 #pragma unroll
@@ -187,29 +224,43 @@ __device__ __forceinline__ uint2 quant_oct(const float (&f)[8], const BlockScale
 }
 
 template <bool kVec>
-__device__ __forceinline__ void store_q(uint8_t* p, int64_t row0, int col, int cols, uint2 q) {
-  if (col >= cols) return;
+__device__ __forceinline__ void store_q(uint8_t* p, const Place& at, int cols, uint2 q) {
   if (kVec) {
-    *reinterpret_cast<uint2*>(p + row0 + col) = q;
+    if (at.col0 < cols) *reinterpret_cast<uint2*>(p + at.row0 + at.col0) = q;
   } else {
 #pragma unroll
-    for (int i = 0; i < 8; ++i)
-      if (col + i < cols) p[row0 + col + i] = static_cast<uint8_t>((i < 4 ? q.x : q.y) >> (8 * (i & 3)));
+    for (int k = 0; k < 8; ++k)
+      if (place_col(at, k) < cols) p[place_at(at, k)] = static_cast<uint8_t>((k < 4 ? q.x : q.y) >> (8 * (k & 3)));
   }
 }
 
-__device__ __forceinline__ float oct_amax(const float (&f)[8]) {
-  float m = 0.f;
+// Scales of the block (kVec) or the two blocks of a lane's elements.  kVec: the 16 lanes of a
+// half warp own a block; else the whole warp owns both.
+template <bool kVec>
+__device__ __forceinline__ void lane_scales(const float (&f)[8], BlockScale& b0, BlockScale& b1) {
+  if (kVec) {
+    float m = 0.f;
 #pragma unroll
-  for (int i = 0; i < 8; ++i) m = fmaxf(m, fabsf(f[i]));
-  return m;
-}
-
-// Maximum over the 16 lanes of a half warp (one 128-column block).
-__device__ __forceinline__ float half_warp_max(float m) {
+    for (int i = 0; i < 8; ++i) m = fmaxf(m, fabsf(f[i]));
 #pragma unroll
-  for (int o = 8; o > 0; o >>= 1) m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, o));
-  return m;
+    for (int o = 8; o > 0; o >>= 1) m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, o));
+    b0 = block_scale(m);
+    b1 = b0;
+  } else {
+    float m0 = 0.f, m1 = 0.f;
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      m0 = fmaxf(m0, fabsf(f[i]));
+      m1 = fmaxf(m1, fabsf(f[i + 4]));
+    }
+#pragma unroll
+    for (int o = 16; o > 0; o >>= 1) {
+      m0 = fmaxf(m0, __shfl_xor_sync(0xffffffffu, m0, o));
+      m1 = fmaxf(m1, __shfl_xor_sync(0xffffffffu, m1, o));
+    }
+    b0 = block_scale(m0);
+    b1 = block_scale(m1);
+  }
 }
 
 // ---------------------------------------------------------------------------
@@ -219,32 +270,44 @@ __device__ __forceinline__ float half_warp_max(float m) {
 // ---------------------------------------------------------------------------
 
 template <bool kXBf16, int kRes, int kOcts, bool kVec>  // kRes: 0 none, 1 fp32, 2 bf16
-__global__ void __launch_bounds__(1024) rms_norm_kernel(RmsNormArgs a) {
-  using XT = typename OctOf<kXBf16>::type;
-  using RT = typename OctOf<kRes == 2>::type;
+__global__ void __launch_bounds__(kOcts == 2 ? 704 : 1024, kOcts == 2 ? 2 : 1) rms_norm_kernel(RmsNormArgs a) {
+  using XT = typename OctOf<kXBf16, kVec>::type;
+  using RT = typename OctOf<kRes == 2, kVec>::type;
   __shared__ float partial[32];
   const int64_t row = static_cast<int64_t>(blockIdx.x) * blockDim.y + threadIdx.y;
   if (row >= a.rows) return;  // whole warps (blockDim.y > 1 only for one-warp teams)
   const int cols = a.cols;
+  const int lane = threadIdx.x & 31;
+  // Octs i * blockDim.x + threadIdx.x of the row, or (not kVec) the warp's 256 columns.
+  auto place = [&](int64_t ld, int i) {
+    Place p;
+    const int oct = threadIdx.x + i * blockDim.x;
+    p.row0 = p.row1 = row * ld;
+    p.col0 = kVec ? oct * 8 : (oct - lane) * 8 + lane;
+    p.col1 = p.col0 + 128;
+    return p;
+  };
   XT xr[kOcts];
   RT rr[kOcts];
-  Bf16Oct wr[kOcts];
 #pragma unroll
   for (int i = 0; i < kOcts; ++i) {
-    const int col = (threadIdx.x + i * blockDim.x) * 8;
     if constexpr (kXBf16)
-      xr[i] = load_oct<kVec>(static_cast<const uint16_t*>(a.x), row * a.ldx, col, cols);
+      xr[i] = load_oct<kVec>(static_cast<const uint16_t*>(a.x), place(a.ldx, i), cols);
     else
-      xr[i] = load_oct<kVec>(static_cast<const float*>(a.x), row * a.ldx, col, cols);
+      xr[i] = load_oct<kVec>(static_cast<const float*>(a.x), place(a.ldx, i), cols);
     if constexpr (kRes == 2)
-      rr[i] = load_oct<kVec, true>(static_cast<const uint16_t*>(a.residual), row * a.ldr, col, cols);
+      rr[i] = load_oct<kVec, true>(static_cast<const uint16_t*>(a.residual), place(a.ldr, i), cols);
     else if constexpr (kRes == 1)
-      rr[i] = load_oct<kVec, true>(static_cast<const float*>(a.residual), row * a.ldr, col, cols);
+      rr[i] = load_oct<kVec, true>(static_cast<const float*>(a.residual), place(a.ldr, i), cols);
   }
+  Place col_place[kOcts];
+#pragma unroll
+  for (int i = 0; i < kOcts; ++i) col_place[i] = place(0, i);
+  typename OctOf<true, kVec>::type wr[kOcts];
   if (a.weight && a.w_bf16) {
 #pragma unroll
     for (int i = 0; i < kOcts; ++i)
-      wr[i] = load_oct<kVec, true>(static_cast<const uint16_t*>(a.weight), 0, (threadIdx.x + i * blockDim.x) * 8, cols);
+      wr[i] = load_oct<kVec, true>(static_cast<const uint16_t*>(a.weight), col_place[i], cols);
   }
   float h[kOcts][8];
   float ss = 0.f;
@@ -264,11 +327,10 @@ __global__ void __launch_bounds__(1024) rms_norm_kernel(RmsNormArgs a) {
     if (a.sum) {
 #pragma unroll
       for (int i = 0; i < kOcts; ++i) {
-        const int col = (threadIdx.x + i * blockDim.x) * 8;
         if constexpr (kRes == 2)
-          store_oct<kVec>(static_cast<uint16_t*>(a.sum), row * a.lds, col, cols, h[i]);
+          store_oct<kVec>(static_cast<uint16_t*>(a.sum), place(a.lds, i), cols, h[i]);
         else
-          store_oct<kVec>(static_cast<float*>(a.sum), row * a.lds, col, cols, h[i]);
+          store_oct<kVec>(static_cast<float*>(a.sum), place(a.lds, i), cols, h[i]);
       }
     }
   }
@@ -277,17 +339,15 @@ __global__ void __launch_bounds__(1024) rms_norm_kernel(RmsNormArgs a) {
   for (int o = 16; o > 0; o >>= 1) ss += __shfl_xor_sync(0xffffffffu, ss, o);
   if (blockDim.x > 32) {
     // One partial per warp; every warp adds them in the same order.
-    if ((threadIdx.x & 31) == 0) partial[threadIdx.x >> 5] = ss;
+    if (lane == 0) partial[threadIdx.x >> 5] = ss;
     __syncthreads();
-    const int lane = threadIdx.x & 31;
     ss = lane < static_cast<int>(blockDim.x >> 5) ? partial[lane] : 0.f;
 #pragma unroll
     for (int o = 16; o > 0; o >>= 1) ss += __shfl_xor_sync(0xffffffffu, ss, o);
   }
-  const float inv = 1.0f / sqrtf(ss / static_cast<float>(cols) + a.eps);
+  const float inv = rsqrtf(fmaf(ss, a.inv_cols, a.eps));  // rsqrtf: within 2 units
 #pragma unroll
   for (int i = 0; i < kOcts; ++i) {
-    const int col = (threadIdx.x + i * blockDim.x) * 8;
 #pragma unroll
     for (int k = 0; k < 8; ++k) h[i][k] = __fmul_rn(h[i][k], inv);
     if (a.weight) {
@@ -295,16 +355,21 @@ __global__ void __launch_bounds__(1024) rms_norm_kernel(RmsNormArgs a) {
       if (a.w_bf16)
         unpack(wr[i], w);
       else
-        unpack(load_oct<kVec, true>(static_cast<const float*>(a.weight), 0, col, cols), w);
+        unpack(load_oct<kVec, true>(static_cast<const float*>(a.weight), col_place[i], cols), w);
 #pragma unroll
       for (int k = 0; k < 8; ++k) h[i][k] = __fmul_rn(h[i][k], w[k]);
     }
-    if (a.y) store_oct<kVec>(a.y, row * a.ldy, col, cols, h[i]);
+    if (a.y) store_oct<kVec>(a.y, place(a.ldy, i), cols, h[i]);
     if (a.q) {
-      const BlockScale b = block_scale(half_warp_max(oct_amax(h[i])));
-      store_q<kVec>(a.q, row * a.ldq, col, cols, quant_oct(h[i], b));
-      if ((threadIdx.x & 15) == 0 && col < cols)
-        a.scale[row * a.blocks + (col >> 7)] = b.s;
+      BlockScale b0, b1;
+      lane_scales<kVec>(h[i], b0, b1);
+      const Place p = place(a.ldq, i);
+      store_q<kVec>(a.q, p, cols, quant_oct(h[i], b0, b1));
+      if ((lane & 15) == 0) {
+        // kVec: lanes 0 and 16 hold the two blocks' scales; else both do
+        const int col = kVec ? p.col0 : p.col0 - lane + 8 * lane;
+        if (col < cols) a.scale[row * a.blocks + (col >> 7)] = kVec || lane == 0 ? b0.s : b1.s;
+      }
     }
   }
 }
@@ -319,7 +384,8 @@ cudaError_t launch_norm_octs(const RmsNormArgs& a, bool vec, dim3 grid, dim3 blo
 }
 
 template <bool kXBf16, int kRes>
-cudaError_t launch_norm(const RmsNormArgs& a, bool vec, cudaStream_t st) {
+cudaError_t launch_norm(RmsNormArgs a, bool vec, cudaStream_t st) {
+  a.inv_cols = 1.0f / static_cast<float>(a.cols);
   const int octs = (a.cols + 7) / 8;
   if (octs <= 128) {  // up to 1024 columns: a warp per row, no shared memory
     const dim3 block(32, a.rows >= 8 ? 8 : static_cast<unsigned>(a.rows));
@@ -329,7 +395,7 @@ cudaError_t launch_norm(const RmsNormArgs& a, bool vec, cudaStream_t st) {
     return launch_norm_octs<kXBf16, kRes, 4>(a, vec, grid, block, st);
   }
   const dim3 grid(static_cast<unsigned>(a.rows));
-  const int per = octs <= 1024 ? (octs <= 512 && a.rows > 296 ? 2 : 1) : octs <= 2048 ? 2 : 4;
+  const int per = octs <= 1024 ? (octs <= 512 && a.rows > 296 ? 2 : 1) : octs <= 1408 ? 2 : 4;
   const dim3 block(static_cast<unsigned>(((octs + per - 1) / per + 31) / 32 * 32));
   if (per == 1) return launch_norm_octs<kXBf16, kRes, 1>(a, vec, grid, block, st);
   if (per == 2) return launch_norm_octs<kXBf16, kRes, 2>(a, vec, grid, block, st);
@@ -345,33 +411,69 @@ bool aligned_to(const void* p, uintptr_t a) { return reinterpret_cast<uintptr_t>
 
 constexpr int kUnits = 4;
 
+// silu(f) = f / (1 + exp(-f)), from the hardware's exponential and reciprocal: relative error
+// below 2^-21 + |f| 2^-23 (the argument f log2(e) is rounded once; ex2 and rcp are within 2
+// units).  With the library's expf and division the kernel was bound by its instructions:
+// 33 per element, 217 us for 16384 x 11008 where the memory takes 139.  exp(-f) = inf gives
+// f * 0 = -0, the limit.
+__device__ __forceinline__ float silu(float f) {
+  float e, r;
+  asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(e) : "f"(__fmul_rn(f, -1.44269504088896341f)));
+  asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(r) : "f"(__fadd_rn(1.0f, e)));
+  return __fmul_rn(f, r);
+}
+
 template <bool kXBf16, bool kGated, bool kVec>
 __global__ void __launch_bounds__(256) row_quant_kernel(RowQuantArgs a) {
-  using XT = typename OctOf<kXBf16>::type;
-  const int64_t half = (static_cast<int64_t>(blockIdx.x) * blockDim.x + threadIdx.x) >> 4;
-  const int lane = threadIdx.x & 15;
+  using XT = typename OctOf<kXBf16, kVec>::type;
+  // Unit u is block u % blocks of row u / blocks.  A warp takes 2 kUnits consecutive units;
+  // step i of its lanes: kVec, unit first + i of its half; else units first + 2 i and + 2 i + 1.
+  const int64_t warp = (static_cast<int64_t>(blockIdx.x) * blockDim.x + threadIdx.x) >> 5;
+  const int lane = threadIdx.x & 31;
   const int64_t units = a.rows * a.blocks;
-  const int64_t first = half * kUnits;
-  if ((half & ~int64_t(1)) * kUnits >= units) return;  // both halves of the warp are past the end
-  int64_t row = first / a.blocks;
+  const int64_t warp_first = warp * (2 * kUnits);
+  if (warp_first >= units) return;
+  const int64_t first = warp_first + (kVec ? (lane >> 4) * kUnits : 0);
+  int64_t row;
+  if (units < (1ll << 31))
+    row = static_cast<uint32_t>(first) / static_cast<uint32_t>(a.blocks);
+  else
+    row = first / a.blocks;
   int blk = static_cast<int>(first - row * a.blocks);
+  auto next = [&](int64_t& r, int& b) {
+    if (++b == a.blocks) {
+      b = 0;
+      ++r;
+    }
+  };
   XT xr[kUnits];
-  Bf16Oct br[kUnits];
-  int64_t rows[kUnits];
-  int cols[kUnits];
+  typename OctOf<true, kVec>::type gr[kUnits];
+  int64_t rows0[kUnits], rows1[kUnits];
+  int cols0[kUnits], cols1[kUnits];
+  const int off = kVec ? (lane & 15) * 8 : lane;
 #pragma unroll
   for (int i = 0; i < kUnits; ++i) {
-    rows[i] = row;
     // past the end: a column that no load or store takes
-    cols[i] = first + i < units ? blk * 128 + lane * 8 : a.cols;
+    const int64_t u = first + (kVec ? i : 2 * i);
+    rows0[i] = row;
+    cols0[i] = u < units ? blk * 128 + off : a.cols;
+    next(row, blk);
+    if (!kVec) {
+      rows1[i] = row;
+      cols1[i] = u + 1 < units ? blk * 128 + off : a.cols;
+      next(row, blk);
+    } else {
+      rows1[i] = rows0[i];
+      cols1[i] = cols0[i];
+    }
+    const Place px = {rows0[i] * a.ldx, rows1[i] * a.ldx, cols0[i], cols1[i]};
     if constexpr (kXBf16)
-      xr[i] = load_oct<kVec>(static_cast<const uint16_t*>(a.x), row * a.ldx, cols[i], a.cols);
+      xr[i] = load_oct<kVec>(static_cast<const uint16_t*>(a.x), px, a.cols);
     else
-      xr[i] = load_oct<kVec>(static_cast<const float*>(a.x), row * a.ldx, cols[i], a.cols);
-    if constexpr (kGated) br[i] = load_oct<kVec>(a.gate, row * a.ldg, cols[i], a.cols);
-    if (++blk == a.blocks) {
-      blk = 0;
-      ++row;
+      xr[i] = load_oct<kVec>(static_cast<const float*>(a.x), px, a.cols);
+    if constexpr (kGated) {
+      const Place pg = {rows0[i] * a.ldg, rows1[i] * a.ldg, cols0[i], cols1[i]};
+      gr[i] = load_oct<kVec>(a.gate, pg, a.cols);
     }
   }
 #pragma unroll
@@ -380,65 +482,78 @@ __global__ void __launch_bounds__(256) row_quant_kernel(RowQuantArgs a) {
     unpack(xr[i], f);
     if constexpr (kGated) {
       float g[8];
-      unpack(br[i], g);
-      // silu(f) = f / (1 + exp(-f)): exp(-f) = inf gives -0, as the limit is
+      unpack(gr[i], g);
 #pragma unroll
-      for (int k = 0; k < 8; ++k) f[k] = __fmul_rn(__fdividef(f[k], 1.0f + expf(-f[k])), g[k]);
+      for (int k = 0; k < 8; ++k) f[k] = __fmul_rn(silu(f[k]), g[k]);
     }
-    const BlockScale b = block_scale(half_warp_max(oct_amax(f)));
-    store_q<kVec>(a.q, rows[i] * a.ldq, cols[i], a.cols, quant_oct(f, b));
-    if (lane == 0 && cols[i] < a.cols) a.scale[first + i] = b.s;
+    BlockScale b0, b1;
+    lane_scales<kVec>(f, b0, b1);
+    const Place pq = {rows0[i] * a.ldq, rows1[i] * a.ldq, cols0[i], cols1[i]};
+    store_q<kVec>(a.q, pq, a.cols, quant_oct(f, b0, b1));
+    if (kVec) {
+      if ((lane & 15) == 0 && cols0[i] < a.cols) a.scale[first + i] = b0.s;
+    } else if ((lane & 15) == 0) {
+      const int64_t u = first + 2 * i + (lane >> 4);
+      if (u < units) a.scale[u] = lane == 0 ? b0.s : b1.s;
+    }
   }
 }
 
 // ---------------------------------------------------------------------------
 // Weight quantiser: a CTA per 128 x 128 tile.  Thread t owns the oct t % 16 of the
-// rows t / 16 + 16 i, i < 8, in registers between the tile's maximum and the store.
+// rows t / 16 + 32 i, i < 4, in registers between the tile's maximum and the store.
 // ---------------------------------------------------------------------------
 
 template <bool kXBf16, bool kVec>
-__global__ void __launch_bounds__(256) tile_quant_kernel(TileQuantArgs a) {
-  using XT = typename OctOf<kXBf16>::type;
-  __shared__ float partial[8];
+__global__ void __launch_bounds__(512, 2) tile_quant_kernel(TileQuantArgs a) {
+  using XT = typename OctOf<kXBf16, kVec>::type;
+  __shared__ float partial[16];
   const int64_t tile = blockIdx.x;
   const int64_t per_mat = static_cast<int64_t>(a.row_blocks) * a.blocks;
   const int64_t mat = tile / per_mat;
   const int rb = static_cast<int>((tile - mat * per_mat) / a.blocks);
   const int cb = static_cast<int>(tile - mat * per_mat - static_cast<int64_t>(rb) * a.blocks);
-  const int col = cb * 128 + (threadIdx.x & 15) * 8;
-  XT xr[8];
+  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+  // kVec: oct t % 16 of row t / 16 + 32 i; else rows 2 warp and 2 warp + 1 (+ 32 i), strided columns
+  auto place = [&](int64_t ld, int i) {
+    const int64_t r0 = static_cast<int64_t>(rb) * 128 + 32 * i + (kVec ? static_cast<int>(threadIdx.x >> 4) : 2 * warp);
+    const int col = cb * 128 + (kVec ? static_cast<int>(threadIdx.x & 15) * 8 : lane);
+    Place p;  // a row past the end: a column that no load or store takes
+    p.row0 = (mat * a.rows + r0) * ld;
+    p.row1 = p.row0 + ld;
+    p.col0 = r0 < a.rows ? col : a.cols;
+    p.col1 = r0 + 1 < a.rows ? col : a.cols;
+    return p;
+  };
+  XT xr[4];
 #pragma unroll
-  for (int i = 0; i < 8; ++i) {
-    const int64_t r = static_cast<int64_t>(rb) * 128 + (threadIdx.x >> 4) + 16 * i;
-    const int c = r < a.rows ? col : a.cols;  // a row past the end reads as 0
-    const int64_t row0 = (mat * a.rows + r) * a.ldx;
+  for (int i = 0; i < 4; ++i) {
     if constexpr (kXBf16)
-      xr[i] = load_oct<kVec>(static_cast<const uint16_t*>(a.x), row0, c, a.cols);
+      xr[i] = load_oct<kVec>(static_cast<const uint16_t*>(a.x), place(a.ldx, i), a.cols);
     else
-      xr[i] = load_oct<kVec>(static_cast<const float*>(a.x), row0, c, a.cols);
+      xr[i] = load_oct<kVec>(static_cast<const float*>(a.x), place(a.ldx, i), a.cols);
   }
   float m = 0.f;
 #pragma unroll
-  for (int i = 0; i < 8; ++i) {
+  for (int i = 0; i < 4; ++i) {
     float f[8];
     unpack(xr[i], f);
-    m = fmaxf(m, oct_amax(f));
+#pragma unroll
+    for (int k = 0; k < 8; ++k) m = fmaxf(m, fabsf(f[k]));
   }
 #pragma unroll
   for (int o = 16; o > 0; o >>= 1) m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, o));
-  if ((threadIdx.x & 31) == 0) partial[threadIdx.x >> 5] = m;
+  if (lane == 0) partial[warp] = m;
   __syncthreads();
   m = 0.f;
 #pragma unroll
-  for (int i = 0; i < 8; ++i) m = fmaxf(m, partial[i]);
+  for (int i = 0; i < 16; ++i) m = fmaxf(m, partial[i]);
   const BlockScale b = block_scale(m);
 #pragma unroll
-  for (int i = 0; i < 8; ++i) {
-    const int64_t r = static_cast<int64_t>(rb) * 128 + (threadIdx.x >> 4) + 16 * i;
-    if (r >= a.rows) continue;
+  for (int i = 0; i < 4; ++i) {
     float f[8];
     unpack(xr[i], f);
-    store_q<kVec>(a.q, (mat * a.rows + r) * a.ldq, col, a.cols, quant_oct(f, b));
+    store_q<kVec>(a.q, place(a.ldq, i), a.cols, quant_oct(f, b, b));
   }
   if (threadIdx.x == 0) a.scale[tile] = b.s;
 }
@@ -466,8 +581,8 @@ cudaError_t launch_rms_norm(const RmsNormArgs& a, cudaStream_t st) {
 cudaError_t launch_row_quant(const RowQuantArgs& a, cudaStream_t st) {
   const bool vec = a.cols % 8 == 0 && aligned_to(a.x, 16) && a.ldx % (a.x_bf16 ? 8 : 4) == 0 &&
                    (!a.gate || (aligned_to(a.gate, 16) && a.ldg % 8 == 0)) && aligned_to(a.q, 8) && a.ldq % 8 == 0;
-  const int64_t halves = (a.rows * a.blocks + kUnits - 1) / kUnits;
-  const unsigned grid = static_cast<unsigned>((halves + 15) / 16);
+  const int64_t warps = (a.rows * a.blocks + 2 * kUnits - 1) / (2 * kUnits);
+  const unsigned grid = static_cast<unsigned>((warps + 7) / 8);
 #define AR_ROW_QUANT(BF, GATED)                                   \
   do {                                                            \
     if (vec)                                                      \
@@ -491,14 +606,14 @@ cudaError_t launch_tile_quant(const TileQuantArgs& a, cudaStream_t st) {
   const unsigned grid = static_cast<unsigned>(a.count * a.row_blocks * a.blocks);
   if (a.x_bf16) {
     if (vec)
-      tile_quant_kernel<true, true><<<grid, 256, 0, st>>>(a);
+      tile_quant_kernel<true, true><<<grid, 512, 0, st>>>(a);
     else
-      tile_quant_kernel<true, false><<<grid, 256, 0, st>>>(a);
+      tile_quant_kernel<true, false><<<grid, 512, 0, st>>>(a);
   } else {
     if (vec)
-      tile_quant_kernel<false, true><<<grid, 256, 0, st>>>(a);
+      tile_quant_kernel<false, true><<<grid, 512, 0, st>>>(a);
     else
-      tile_quant_kernel<false, false><<<grid, 256, 0, st>>>(a);
+      tile_quant_kernel<false, false><<<grid, 512, 0, st>>>(a);
   }
   return cudaGetLastError();
 }
