@@ -287,24 +287,30 @@ __global__ void __launch_bounds__(kOcts == 2 ? 704 : 1024, kOcts == 2 ? 2 : 1) r
     p.col1 = p.col0 + 128;
     return p;
   };
-  XT xr[kOcts];
-  RT rr[kOcts];
-#pragma unroll
-  for (int i = 0; i < kOcts; ++i) {
+  // Every load of the thread is issued before the first value is used (unaligned rows take eight
+  // loads an oct: there an oct's are).
+  constexpr int kAhead = kVec ? kOcts : 1;
+  XT xr[kAhead];
+  RT rr[kAhead];
+  auto load = [&](int i, int at) {
     if constexpr (kXBf16)
-      xr[i] = load_oct<kVec>(static_cast<const uint16_t*>(a.x), place(a.ldx, i), cols);
+      xr[at] = load_oct<kVec>(static_cast<const uint16_t*>(a.x), place(a.ldx, i), cols);
     else
-      xr[i] = load_oct<kVec>(static_cast<const float*>(a.x), place(a.ldx, i), cols);
+      xr[at] = load_oct<kVec>(static_cast<const float*>(a.x), place(a.ldx, i), cols);
     if constexpr (kRes == 2)
-      rr[i] = load_oct<kVec, true>(static_cast<const uint16_t*>(a.residual), place(a.ldr, i), cols);
+      rr[at] = load_oct<kVec, true>(static_cast<const uint16_t*>(a.residual), place(a.ldr, i), cols);
     else if constexpr (kRes == 1)
-      rr[i] = load_oct<kVec, true>(static_cast<const float*>(a.residual), place(a.ldr, i), cols);
+      rr[at] = load_oct<kVec, true>(static_cast<const float*>(a.residual), place(a.ldr, i), cols);
+  };
+  if constexpr (kVec) {
+#pragma unroll
+    for (int i = 0; i < kOcts; ++i) load(i, i);
   }
   Place col_place[kOcts];
 #pragma unroll
   for (int i = 0; i < kOcts; ++i) col_place[i] = place(0, i);
-  typename OctOf<true, kVec>::type wr[kOcts];
-  if (a.weight && a.w_bf16) {
+  Bf16Oct wr[kOcts];
+  if constexpr (kVec) if (a.weight && a.w_bf16) {
 #pragma unroll
     for (int i = 0; i < kOcts; ++i)
       wr[i] = load_oct<kVec, true>(static_cast<const uint16_t*>(a.weight), col_place[i], cols);
@@ -313,10 +319,11 @@ __global__ void __launch_bounds__(kOcts == 2 ? 704 : 1024, kOcts == 2 ? 2 : 1) r
   float ss = 0.f;
 #pragma unroll
   for (int i = 0; i < kOcts; ++i) {
-    unpack(xr[i], h[i]);
+    if constexpr (!kVec) load(i, 0);
+    unpack(xr[kVec ? i : 0], h[i]);
     if constexpr (kRes != 0) {
       float r[8];
-      unpack(rr[i], r);
+      unpack(rr[kVec ? i : 0], r);
 #pragma unroll
       for (int k = 0; k < 8; ++k) h[i][k] = __fadd_rn(h[i][k], r[k]);
     }
@@ -352,8 +359,10 @@ __global__ void __launch_bounds__(kOcts == 2 ? 704 : 1024, kOcts == 2 ? 2 : 1) r
     for (int k = 0; k < 8; ++k) h[i][k] = __fmul_rn(h[i][k], inv);
     if (a.weight) {
       float w[8];
-      if (a.w_bf16)
+      if (kVec && a.w_bf16)
         unpack(wr[i], w);
+      else if (a.w_bf16)
+        unpack(load_oct<kVec, true>(static_cast<const uint16_t*>(a.weight), col_place[i], cols), w);
       else
         unpack(load_oct<kVec, true>(static_cast<const float*>(a.weight), col_place[i], cols), w);
 #pragma unroll
@@ -409,7 +418,10 @@ bool aligned_to(const void* p, uintptr_t a) { return reinterpret_cast<uintptr_t>
 // each, so a thread has kUnits 16-byte loads in flight (twice that with the gate).
 // ---------------------------------------------------------------------------
 
-constexpr int kUnits = 4;
+// Units in flight per half warp.  Unaligned rows are loaded element by element, eight loads a
+// step: one step, and as many warps as fit, keep more of them in flight than four.
+template <bool kVec>
+constexpr int kUnitsOf = kVec ? 4 : 1;
 
 // silu(f) = f / (1 + exp(-f)), from the hardware's exponential and reciprocal: relative error
 // below 2^-21 + |f| 2^-23 (the argument f log2(e) is rounded once; ex2 and rcp are within 2
@@ -426,6 +438,7 @@ __device__ __forceinline__ float silu(float f) {
 template <bool kXBf16, bool kGated, bool kVec>
 __global__ void __launch_bounds__(256) row_quant_kernel(RowQuantArgs a) {
   using XT = typename OctOf<kXBf16, kVec>::type;
+  constexpr int kUnits = kUnitsOf<kVec>;
   // Unit u is block u % blocks of row u / blocks.  A warp takes 2 kUnits consecutive units;
   // step i of its lanes: kVec, unit first + i of its half; else units first + 2 i and + 2 i + 1.
   const int64_t warp = (static_cast<int64_t>(blockIdx.x) * blockDim.x + threadIdx.x) >> 5;
@@ -581,7 +594,8 @@ cudaError_t launch_rms_norm(const RmsNormArgs& a, cudaStream_t st) {
 cudaError_t launch_row_quant(const RowQuantArgs& a, cudaStream_t st) {
   const bool vec = a.cols % 8 == 0 && aligned_to(a.x, 16) && a.ldx % (a.x_bf16 ? 8 : 4) == 0 &&
                    (!a.gate || (aligned_to(a.gate, 16) && a.ldg % 8 == 0)) && aligned_to(a.q, 8) && a.ldq % 8 == 0;
-  const int64_t warps = (a.rows * a.blocks + 2 * kUnits - 1) / (2 * kUnits);
+  const int per_warp = 2 * (vec ? kUnitsOf<true> : kUnitsOf<false>);
+  const int64_t warps = (a.rows * a.blocks + per_warp - 1) / per_warp;
   const unsigned grid = static_cast<unsigned>((warps + 7) / 8);
 #define AR_ROW_QUANT(BF, GATED)                                   \
   do {                                                            \
