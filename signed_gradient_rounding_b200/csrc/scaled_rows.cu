@@ -436,7 +436,7 @@ __device__ __forceinline__ float silu(float f) {
 }
 
 template <bool kXBf16, bool kGated, bool kVec>
-__global__ void __launch_bounds__(256) row_quant_kernel(RowQuantArgs a) {
+__global__ void __launch_bounds__(256, kVec ? 4 : 1) row_quant_kernel(RowQuantArgs a) {
   using XT = typename OctOf<kXBf16, kVec>::type;
   constexpr int kUnits = kUnitsOf<kVec>;
   // Unit u is block u % blocks of row u / blocks.  A warp takes 2 kUnits consecutive units;
@@ -571,6 +571,57 @@ __global__ void __launch_bounds__(512, 2) tile_quant_kernel(TileQuantArgs a) {
   if (threadIdx.x == 0) a.scale[tile] = b.s;
 }
 
+// The same for aligned bf16 rows, the tile in shared memory: a thread copies its eight octs
+// there asynchronously and reads them back twice, so the tile in flight takes no registers
+// and six CTAs share an SM.  (Each thread reads only what it copied.)
+__global__ void __launch_bounds__(256, 6) tile_quant_async_kernel(TileQuantArgs a) {
+  __shared__ uint4 buf[8 * 256];
+  __shared__ float partial[8];
+  const int64_t tile = blockIdx.x;
+  const int64_t per_mat = static_cast<int64_t>(a.row_blocks) * a.blocks;
+  const int64_t mat = tile / per_mat;
+  const int rb = static_cast<int>((tile - mat * per_mat) / a.blocks);
+  const int cb = static_cast<int>(tile - mat * per_mat - static_cast<int64_t>(rb) * a.blocks);
+  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+  const int64_t r0 = static_cast<int64_t>(rb) * 128 + (threadIdx.x >> 4);
+  const int col = cb * 128 + (threadIdx.x & 15) * 8;
+  const bool col_ok = col < a.cols;
+  const uint16_t* x = static_cast<const uint16_t*>(a.x) + (mat * a.rows + r0) * a.ldx + col;
+#pragma unroll
+  for (int i = 0; i < 8; ++i) {
+    const bool ok = col_ok && r0 + 16 * i < a.rows;
+    asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(smem_u32(&buf[i * 256 + threadIdx.x])),
+                 "l"(ok ? x + 16 * i * a.ldx : static_cast<const uint16_t*>(a.x)), "r"(ok ? 16 : 0)
+                 : "memory");
+  }
+  asm volatile("cp.async.wait_all;" ::: "memory");
+  float m = 0.f;
+#pragma unroll
+  for (int i = 0; i < 8; ++i) {
+    float f[8];
+    unpack(Bf16Oct{buf[i * 256 + threadIdx.x]}, f);
+#pragma unroll
+    for (int k = 0; k < 8; ++k) m = fmaxf(m, fabsf(f[k]));
+  }
+#pragma unroll
+  for (int o = 16; o > 0; o >>= 1) m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, o));
+  if (lane == 0) partial[warp] = m;
+  __syncthreads();
+  m = 0.f;
+#pragma unroll
+  for (int i = 0; i < 8; ++i) m = fmaxf(m, partial[i]);
+  const BlockScale b = block_scale(m);
+  uint8_t* q = a.q + (mat * a.rows + r0) * a.ldq + col;
+#pragma unroll
+  for (int i = 0; i < 8; ++i) {
+    float f[8];
+    unpack(Bf16Oct{buf[i * 256 + threadIdx.x]}, f);
+    const uint2 v = quant_oct(f, b, b);
+    if (col_ok && r0 + 16 * i < a.rows) *reinterpret_cast<uint2*>(q + 16 * i * a.ldq) = v;
+  }
+  if (threadIdx.x == 0) a.scale[tile] = b.s;
+}
+
 }  // namespace
 
 cudaError_t launch_rms_norm(const RmsNormArgs& a, cudaStream_t st) {
@@ -620,7 +671,7 @@ cudaError_t launch_tile_quant(const TileQuantArgs& a, cudaStream_t st) {
   const unsigned grid = static_cast<unsigned>(a.count * a.row_blocks * a.blocks);
   if (a.x_bf16) {
     if (vec)
-      tile_quant_kernel<true, true><<<grid, 512, 0, st>>>(a);
+      tile_quant_async_kernel<<<grid, 256, 0, st>>>(a);
     else
       tile_quant_kernel<true, false><<<grid, 512, 0, st>>>(a);
   } else {
