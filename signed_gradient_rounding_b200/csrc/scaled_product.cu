@@ -15,8 +15,6 @@
 //     swizzle, so both operand types share one pipeline.
 //   * skinny_kernel: few rows per expert, bound by the weight's bytes; each weight
 //     byte goes from HBM straight into the registers of the warp that multiplies it.
-#include <stddef.h>
-
 #include <atomic>
 
 #include "ar_device.cuh"
@@ -854,11 +852,31 @@ struct Piece {
 
 constexpr int kSkinnyWarps = 8;
 
-template <bool kF8, int kNT, int kMR, int kU>  // kNT tiles of 8 rows of X per pass, kU K blocks in flight per warp
+// A lane's 16-byte asynchronous copy into its own place (zeros instead where `ok` is false).
+__device__ __forceinline__ void cp_async_own(uint4* dst, const uint8_t* src, bool ok) {
+  asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(smem_u32(dst)), "l"(src), "r"(ok ? 16 : 0) : "memory");
+}
+
+// kNT tiles of 8 rows of X per pass, kMR strips of 16 rows of W per CTA.  Each warp keeps the
+// operands of kS K blocks in flight, in its own part of shared memory: asynchronous copies
+// that each lane makes for itself and reads back itself, so nothing but its own
+// cp.async groups orders them, and the bytes in flight (80 to 160 KB an SM) cost no registers.
+// (With the same loads into registers, one or two blocks ahead, 64 experts of one row each, 4096 ->
+// 2048, took 58.5 us; so they take 51, 90% of the measured copy bandwidth.)
+template <bool kF8, int kNT, int kMR, int kS>
+struct SkinnyCfg {
+  static constexpr int kTok = 8 * kNT, kRows = 16 * kMR;
+  static constexpr int kPieces = kMR * 4 + kNT * 2;  // 16-byte pieces per lane and K block
+  static constexpr int kRing = kSkinnyWarps * kS * kPieces * 32 * 16;
+  static constexpr int kRed = kSkinnyWarps * kTok * (kRows + 1) * 4;  // takes the ring's place after the last block
+  static constexpr int kSmemBytes = kRing > kRed ? kRing : kRed;
+};
+
+template <bool kF8, int kNT, int kMR, int kS>
 __global__ void __launch_bounds__(32 * kSkinnyWarps) skinny_kernel(const __grid_constant__ ProductArgs a) {
-  constexpr int kTok = 8 * kNT;
-  constexpr int kRows = 16 * kMR;
-  __shared__ float red[kSkinnyWarps][kTok][kRows + 1];
+  using C = SkinnyCfg<kF8, kNT, kMR, kS>;
+  constexpr int kTok = C::kTok, kRows = C::kRows;
+  extern __shared__ uint4 skinny_smem[];
   const int e = blockIdx.y;
   int r0, r1;
   expert_rows(a, e, r0, r1);
@@ -870,7 +888,10 @@ __global__ void __launch_bounds__(32 * kSkinnyWarps) skinny_kernel(const __grid_
   const int64_t w_off = (static_cast<int64_t>(e) * a.out + o0 + g) * a.ldw + q * 16;
   // (the rows of a CTA lie in one 128-row scale block: kRows divides 128)
   const float* ws = kF8 ? a.ws + (static_cast<int64_t>(e) * a.out_blocks + (o0 >> 7)) * a.nkb : nullptr;
-  const int segs = (!kF8 && a.W_lo) ? 2 : 1;
+  const int blocks = (!kF8 && a.W_lo) ? 2 * a.nkb : a.nkb;  // the lo half's follow the hi half's
+  // [stage][piece][lane] of this warp
+  uint4* ring = skinny_smem + warp * (kS * C::kPieces * 32) + lane;
+  auto red = reinterpret_cast<float(*)[kTok][kRows + 1]>(skinny_smem);
 
   for (int t0 = r0; t0 < r1; t0 += kTok) {
     float acc[kMR][kNT][4];
@@ -880,95 +901,101 @@ __global__ void __launch_bounds__(32 * kSkinnyWarps) skinny_kernel(const __grid_
       for (int nt = 0; nt < kNT; ++nt)
 #pragma unroll
         for (int i = 0; i < 4; ++i) acc[m][nt][i] = 0.f;
-    for (int seg = 0; seg < segs; ++seg) {
-      const uint8_t* wp = static_cast<const uint8_t*>(seg ? a.W_lo : a.W) + w_off;
-      for (int kb0 = warp; kb0 < a.nkb; kb0 += kU * kSkinnyWarps) {
-        uint4 w[kU][kMR][2][2], x[kU][kNT][2];
-        float sx[kU][kNT][2], sw[kU];
+    float sx[kS][kNT][2], sw[kS];  // the scales of the stages' blocks
+    // Block b into stage j: the copies, and the scales into registers; one group, empty past the end.
+    auto load = [&](int b, int j) {
+      if (b < blocks) {
+        const bool lo = !kF8 && b >= a.nkb;
+        const uint8_t* wp = static_cast<const uint8_t*>(lo ? a.W_lo : a.W) + w_off;
+        const int kb = lo ? b - a.nkb : b;
+        uint4* dst = ring + j * (C::kPieces * 32);
 #pragma unroll
-        for (int j = 0; j < kU; ++j) {
-          const int kb = kb0 + j * kSkinnyWarps;
+        for (int c = 0; c < 2; ++c) {
+          const int k = kb * kKBytes + c * 64;
+          const bool k_ok = k + q * 16 < in_bytes;
 #pragma unroll
-          for (int c = 0; c < 2; ++c) {
-            const int k = kb * kKBytes + c * 64;
-            const bool k_ok = k + q * 16 < in_bytes;  // also false for kb past the end
+          for (int m = 0; m < kMR; ++m)
 #pragma unroll
-            for (int m = 0; m < kMR; ++m)
-#pragma unroll
-              for (int h = 0; h < 2; ++h) {
-                uint4& v = w[j][m][c][h];
-                v = make_uint4(0, 0, 0, 0);
-                if (k_ok && o0 + m * 16 + h * 8 + g < a.out) {
-                  const uint8_t* p = wp + static_cast<int64_t>(m * 16 + h * 8) * a.ldw + k;
-                  asm("ld.global.nc.L1::no_allocate.v4.u32 {%0, %1, %2, %3}, [%4];"
-                      : "=r"(v.x), "=r"(v.y), "=r"(v.z), "=r"(v.w)
-                      : "l"(p));
-                }
-              }
-#pragma unroll
-            for (int nt = 0; nt < kNT; ++nt) {
-              x[j][nt][c] = make_uint4(0, 0, 0, 0);
-              const int row = t0 + nt * 8 + g;
-              if (k_ok && row < r1)
-                x[j][nt][c] = __ldg(reinterpret_cast<const uint4*>(static_cast<const uint8_t*>(a.X) +
-                                                                   static_cast<int64_t>(row) * a.ldx + q * 16 + k));
+            for (int h = 0; h < 2; ++h) {
+              const bool ok = k_ok && o0 + m * 16 + h * 8 + g < a.out;
+              cp_async_own(dst + ((m * 2 + c) * 2 + h) * 32,
+                           ok ? wp + static_cast<int64_t>(m * 16 + h * 8) * a.ldw + k : static_cast<const uint8_t*>(a.W), ok);
             }
+#pragma unroll
+          for (int nt = 0; nt < kNT; ++nt) {
+            const int row = t0 + nt * 8 + g;
+            const bool ok = k_ok && row < r1;
+            const uint8_t* x = static_cast<const uint8_t*>(a.X);
+            cp_async_own(dst + (kMR * 4 + nt * 2 + c) * 32, ok ? x + static_cast<int64_t>(row) * a.ldx + q * 16 + k : x, ok);
           }
-          if (kF8) {
-            const bool kb_ok = kb < a.nkb;
-            sw[j] = kb_ok ? __ldg(ws + kb) : 0.f;
+        }
+        if (kF8) {
+          sw[j] = __ldg(ws + kb);
+#pragma unroll
+          for (int nt = 0; nt < kNT; ++nt)
+#pragma unroll
+            for (int h = 0; h < 2; ++h) {
+              const int row = t0 + nt * 8 + q * 2 + h;
+              sx[j][nt][h] = row < r1 ? __ldg(a.xs + static_cast<int64_t>(row) * a.nkb + kb) : 0.f;
+            }
+        }
+      }
+      asm volatile("cp.async.commit_group;" ::: "memory");
+    };
+#pragma unroll
+    for (int j = 0; j < kS; ++j) load(warp + j * kSkinnyWarps, j);
+    for (int b0 = warp; b0 < blocks; b0 += kS * kSkinnyWarps) {
+#pragma unroll
+      for (int j = 0; j < kS; ++j) {
+        const int b = b0 + j * kSkinnyWarps;
+        if (b >= blocks) break;
+        asm volatile("cp.async.wait_group %0;" ::"n"(kS - 1) : "memory");  // the oldest group: stage j's
+        const uint4* src = ring + j * (C::kPieces * 32);
+        float part[kMR][kNT][4];
+        if (kF8) {
+#pragma unroll
+          for (int m = 0; m < kMR; ++m)
 #pragma unroll
             for (int nt = 0; nt < kNT; ++nt)
 #pragma unroll
-              for (int h = 0; h < 2; ++h) {
-                const int row = t0 + nt * 8 + q * 2 + h;
-                sx[j][nt][h] = kb_ok && row < r1 ? __ldg(a.xs + static_cast<int64_t>(row) * a.nkb + kb) : 0.f;
-              }
-          }
+              for (int i = 0; i < 4; ++i) part[m][nt][i] = 0.f;
         }
 #pragma unroll
-        for (int j = 0; j < kU; ++j) {
-          if (j > 0 && kb0 + j * kSkinnyWarps >= a.nkb) break;  // (a block past the end has no scales)
-          float part[kMR][kNT][4];
-          if (kF8) {
+        for (int c = 0; c < 2; ++c) {
+          uint4 xv[kNT];
 #pragma unroll
-            for (int m = 0; m < kMR; ++m)
+          for (int nt = 0; nt < kNT; ++nt) xv[nt] = src[(kMR * 4 + nt * 2 + c) * 32];
 #pragma unroll
-              for (int nt = 0; nt < kNT; ++nt)
-#pragma unroll
-                for (int i = 0; i < 4; ++i) part[m][nt][i] = 0.f;
-          }
-#pragma unroll
-          for (int c = 0; c < 2; ++c) {
-#pragma unroll
-            for (int m = 0; m < kMR; ++m) {
-              const Piece<kF8> lo(w[j][m][c][0]), hi(w[j][m][c][1]);
-#pragma unroll
-              for (int nt = 0; nt < kNT; ++nt) {
-                const Piece<kF8> xx(x[j][nt][c]);
-#pragma unroll
-                for (int s = 0; s < Piece<kF8>::kSteps; ++s)
-                  mma_16x8<kF8>(kF8 ? part[m][nt] : acc[m][nt], lo.r[s][0], hi.r[s][0], lo.r[s][1], hi.r[s][1],
-                                xx.r[s][0], xx.r[s][1]);
-              }
-            }
-          }
-          if (kF8) {
+          for (int m = 0; m < kMR; ++m) {
+            const Piece<kF8> lo(src[((m * 2 + c) * 2) * 32]), hi(src[((m * 2 + c) * 2 + 1) * 32]);
 #pragma unroll
             for (int nt = 0; nt < kNT; ++nt) {
-              const float s0 = __fmul_rn(sx[j][nt][0], sw[j]), s1 = __fmul_rn(sx[j][nt][1], sw[j]);
+              const Piece<kF8> xx(xv[nt]);
 #pragma unroll
-              for (int m = 0; m < kMR; ++m) {
-                acc[m][nt][0] = fmaf(part[m][nt][0], s0, acc[m][nt][0]);
-                acc[m][nt][1] = fmaf(part[m][nt][1], s1, acc[m][nt][1]);
-                acc[m][nt][2] = fmaf(part[m][nt][2], s0, acc[m][nt][2]);
-                acc[m][nt][3] = fmaf(part[m][nt][3], s1, acc[m][nt][3]);
-              }
+              for (int s = 0; s < Piece<kF8>::kSteps; ++s)
+                mma_16x8<kF8>(kF8 ? part[m][nt] : acc[m][nt], lo.r[s][0], hi.r[s][0], lo.r[s][1], hi.r[s][1],
+                              xx.r[s][0], xx.r[s][1]);
             }
           }
         }
+        if (kF8) {
+#pragma unroll
+          for (int nt = 0; nt < kNT; ++nt) {
+            const float s0 = __fmul_rn(sx[j][nt][0], sw[j]), s1 = __fmul_rn(sx[j][nt][1], sw[j]);
+#pragma unroll
+            for (int m = 0; m < kMR; ++m) {
+              acc[m][nt][0] = fmaf(part[m][nt][0], s0, acc[m][nt][0]);
+              acc[m][nt][1] = fmaf(part[m][nt][1], s1, acc[m][nt][1]);
+              acc[m][nt][2] = fmaf(part[m][nt][2], s0, acc[m][nt][2]);
+              acc[m][nt][3] = fmaf(part[m][nt][3], s1, acc[m][nt][3]);
+            }
+          }
+        }
+        load(b + kS * kSkinnyWarps, j);
       }
     }
+    asm volatile("cp.async.wait_all;" ::: "memory");
+    __syncthreads();  // every warp is done with the ring
     // c0, c1: weight row g, rows 2q and 2q + 1 of X; c2, c3: weight row g + 8.
 #pragma unroll
     for (int m = 0; m < kMR; ++m)
@@ -992,13 +1019,6 @@ __global__ void __launch_bounds__(32 * kSkinnyWarps) skinny_kernel(const __grid_
     }
     __syncthreads();
   }
-}
-
-template <bool kF8, int kNT, int kMR, int kU>
-cudaError_t launch_skinny(const ProductArgs& a, cudaStream_t st) {
-  const dim3 grid((a.out + 16 * kMR - 1) / (16 * kMR), a.experts);
-  skinny_kernel<kF8, kNT, kMR, kU><<<grid, 32 * kSkinnyWarps, 0, st>>>(a);
-  return cudaGetLastError();
 }
 
 // ---------------------------------------------------------------------------
@@ -1025,6 +1045,21 @@ cudaError_t device_info(DeviceInfo* d) {
     sms[d->dev].store(d->sms, std::memory_order_relaxed);
   }
   return cudaSuccess;
+}
+
+template <bool kF8, int kNT, int kMR, int kS>
+cudaError_t launch_skinny(const ProductArgs& a, const DeviceInfo& d, cudaStream_t st) {
+  using C = SkinnyCfg<kF8, kNT, kMR, kS>;
+  auto* fn = skinny_kernel<kF8, kNT, kMR, kS>;
+  static std::atomic<int> ready[64];  // per device: the shared-memory limit is raised
+  if (!ready[d.dev].load(std::memory_order_relaxed)) {
+    const cudaError_t e = cudaFuncSetAttribute(fn, cudaFuncAttributeMaxDynamicSharedMemorySize, C::kSmemBytes);
+    if (e != cudaSuccess) return e;
+    ready[d.dev].store(1, std::memory_order_relaxed);
+  }
+  const dim3 grid((a.out + C::kRows - 1) / C::kRows, a.experts);
+  fn<<<grid, 32 * kSkinnyWarps, C::kSmemBytes, st>>>(a);
+  return cudaGetLastError();
 }
 
 // Units of bm rows x bn columns that can have work (exact for one expert).
@@ -1084,37 +1119,36 @@ cudaError_t launch_tile(ProductArgs a, const DeviceInfo& d, cudaStream_t st, int
   return cudaLaunchKernelEx(&cfg, fn, mx, mw, mlo, a);
 }
 
-// Which kernel.  Both operand types, times on one B200 in us.
+// Which kernel.  Both operand types, times on one B200 in us (e4m3 unless said).
 //
 // Rows per expert (on average) decide between the two kernels.  The skinny one has no
 // fixed cost but walks W again for every kTok rows; the tile one starts at 8 us (tensor
 // memory, barriers, descriptors, the first loads) and then takes 128 rows for the price of one.
-//   n = 1,  4096 -> 4096:  skinny 6.5, tile 12        n = 32, 4096 -> 4096:  skinny 10.9, tile 12.4
-//   n = 16, 29568 -> 8192: skinny 56, tile 63         n = 32, 29568 -> 8192: skinny 104, tile 62
-//   64 experts, 2048 -> 1024, 4 rows each: 30 and 38; 8 rows: 38 and 38; 16 rows: 50 and 39
-// Several experts are taken to be uneven (some have several times the average).
+//   n = 8,  29568 -> 8192: skinny 43, tile 62         n = 16, 29568 -> 8192: skinny 48, tile 50
+//   n = 32, 4096 -> 4096:  skinny 10, tile 11.2       n = 32, 29568 -> 8192: skinny 87, tile 49
+//   n = 32, 4096 -> 11008: skinny 21, tile 18         n = 64, 4096 -> 4096:  skinny 17, tile 12
+// Several experts are taken to be uneven (some have several times the average):
+//   64 experts, 4096 -> 2048, 4 rows each: 83 and 115; 8: 102 and 107; 12: 117 and 108
+//   the same in bf16, 8 rows each: 187 and 183; 12: 220 and 184
+// Of the skinny kernel's shapes, two strips of W per CTA and two blocks per warp in flight won
+// over one strip (51 and 69 for 64 experts with 64 rows) and over more blocks (three: 70;
+// shared memory then holds fewer CTAs); 8 rows of X per pass while there are no more, 16 up to 16.
 //
 // Among the tiles, 128 x 128 on one SM, 128 x 256 on one SM and 256 x 256 on a pair, the
 // fewest waves times the cost of a wave: e4m3, K = 4096: 16, 26.5 and 25 us a wave (n = 16384,
 // 4096 -> 11008: 1157, 1022, 933 in all; n = 333: 35, 28, 56; n = 512, 4096 -> 4096: 19, 26, 25);
 // bf16: 13, 21 and 20 for 2048 columns of K.  With half the SMs idle or more, 128 x 128
-// tiles share their K blocks among a cluster of 2 or 4 CTAs (n = 64, 4096 -> 4096: 19 alone,
-// 16 and 12.8 shared; 29568 -> 8192: 104, 61).  A cluster of 8 gained nothing more (7.6 for
+// tiles share their K blocks among a cluster of 2 or 4 CTAs (n = 64, 4096 -> 4096: 17.5 alone,
+// 13.8 and 12.2 shared; 29568 -> 8192: 85, 50).  A cluster of 8 gained nothing more (7.6 for
 // 7.7 at 1024 -> 1000) and lost up to twice the time.
 template <bool kF8>
 cudaError_t launch_type(const ProductArgs& a, const DeviceInfo& d, cudaStream_t st) {
   const int64_t per = (static_cast<int64_t>(a.n) + a.experts - 1) / a.experts;
   const int64_t strips = (a.out + 15) / 16;  // 16-row strips of one W
-  if (per <= 8) {
-    // Two strips per CTA halve the conversions of X, where enough CTAs are left (e4m3 only:
-    // 29568 -> 8192 56 -> 50; bf16 operands need none).
-    if (kF8 && strips / 2 * a.experts >= d.sms * 3 / 2) return launch_skinny<kF8, 1, 2, 1>(a, st);
-    return launch_skinny<kF8, 1, 1, 2>(a, st);
-  }
-  if (a.experts == 1) {
-    if (per <= 16) return launch_skinny<kF8, 2, 2, 1>(a, st);
-    if (per <= 64 && (per + 31) / 32 * strips * a.nkb <= 8192) return launch_skinny<kF8, 4, 1, 1>(a, st);
-  }
+  const bool one = a.experts == 1;
+  if (per <= (one ? 8 : 4)) return launch_skinny<kF8, 1, 2, 2>(a, d, st);
+  if (per <= (one ? 16 : 8)) return launch_skinny<kF8, 2, 2, 2>(a, d, st);
+  if (one && per <= 64 && (per + 31) / 32 * strips * a.nkb <= 8192) return launch_skinny<kF8, 4, 1, 2>(a, d, st);
   // Row blocks: exact for one expert, else half a block more per expert, and one at least.
   const int64_t active = a.experts < a.n ? a.experts : a.n;
   auto waves = [&](int bm, int bn, int resident) {
