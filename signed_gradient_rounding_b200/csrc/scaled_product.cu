@@ -140,78 +140,64 @@ __device__ __forceinline__ uint32_t pack2(float lo, float hi) {
   return *reinterpret_cast<const uint32_t*>(&h);
 }
 
-// Columns [col, col + 8) of row `row` of Y: + add, one rounding to bf16.
-__device__ __forceinline__ void store8(const ProductArgs& a, int64_t row, int col, float (&x)[8]) {
-  if (col >= a.out) return;
-  uint16_t* y = a.Y + row * a.ldy + col;
-  const uint16_t* add = a.add ? a.add + row * a.ldadd + col : nullptr;
-  if (a.vec_y && col + 8 <= a.out) {
-    if (add) {
-      const uint4 v = *reinterpret_cast<const uint4*>(add);
-      const uint32_t w[4] = {v.x, v.y, v.z, v.w};
-#pragma unroll
-      for (int i = 0; i < 4; ++i) {
-        x[2 * i] += __uint_as_float(w[i] << 16);
-        x[2 * i + 1] += __uint_as_float(w[i] & 0xFFFF0000u);
-      }
-    }
-    *reinterpret_cast<uint4*>(y) =
-        make_uint4(pack2(x[0], x[1]), pack2(x[2], x[3]), pack2(x[4], x[5]), pack2(x[6], x[7]));
-  } else {
-#pragma unroll
-    for (int i = 0; i < 8; ++i) {
-      if (col + i >= a.out) break;
-      const float v = add ? x[i] + bf16_bits_to_f32(add[i]) : x[i];
-      y[i] = static_cast<uint16_t>(pack2(v, 0.f) & 0xFFFFu);
-    }
-  }
-}
-
-// The way out of a warp's 32 rows x kNC columns (lane = row; rows from r1 on belong to
-// others): each lane rounds its row's values into its own line of shared memory (put8) and
-// sends the line to Y with one bulk copy (send), which runs while the warp goes on with the
-// next unit.  (Stored from registers, 16 bytes of 32 rows per instruction, the columns of a
-// 256 x 256 tile kept the warps for 7500 cycles; through shared memory with coalesced
-// stores for 3700, since every SM writes at the same time.)
+// The way out of a warp's 32 rows x up to kNC columns (lane = row; rows from r1 on belong to
+// others): each lane rounds its row's values into its own line of shared memory (put8), and
+// the lines go to Y (send): each by one bulk copy, which runs while the warp goes on with the
+// next unit, or, where Y's rows are not 16-byte aligned, by the whole warp element by
+// element.  The residual comes the same way back, asked for at the unit's start (begin).
+// (Stored from registers, 16 bytes of 32 rows per instruction, the columns of a 256 x 256 tile
+// kept the warps for 7500 cycles; through shared memory with coalesced stores for 3700, since
+// every SM writes at the same time.  Element by element from registers, 667 rows of 944 -> 3689
+// took 54 us.)
 template <int kNC>
 struct RowsOut {
-  uint8_t* line;    // this lane's line
-  int row, r1, col; // this lane's row; first column
-  int cols;         // columns that exist, at most kNC
-  bool bulk;        // whole 16-byte units at aligned addresses: the bulk copy; else direct stores
+  static constexpr int kPitch = kNC * 2 + 16;
+  uint8_t* lines;    // the warp's lines
+  int row0, r1, col; // first row, end of the rows that exist, first column
+  int cols;          // columns that exist (0 or fewer: none)
+  int lane;
+  bool bulk;         // whole 16-byte units at aligned addresses
 
-  __device__ __forceinline__ void begin(const ProductArgs& a, uint8_t* warp_buf, int row0, int r1_, int col_, int lane) {
-    constexpr int kPitch = kNC * 2 + 16;
-    line = warp_buf + lane * kPitch;
-    row = row0 + lane;
+  __device__ __forceinline__ void begin(const ProductArgs& a, uint8_t* warp_lines, int row0_, int r1_, int col_,
+                                        int width, int lane_) {
+    lines = warp_lines;
+    row0 = row0_;
     r1 = r1_;
     col = col_;
-    cols = min(kNC, a.out - col);
+    lane = lane_;
+    cols = min(width, a.out - col);
     bulk = a.vec_y && cols % 8 == 0;
-    asm volatile("cp.async.bulk.wait_group.read 0;" ::: "memory");  // the last unit's copy has read the line
+    asm volatile("cp.async.bulk.wait_group.read 0;" ::: "memory");  // the last unit's copies have read the lines
     __syncwarp();  // (every lane's: the residual is brought in by the whole warp)
-    if (a.add && bulk) {
-      // the residual, coalesced, into the lines
-      constexpr int kUnits = kNC / 8;  // 16-byte units per row
+    if (!a.add) return;
+    if (bulk) {
+      constexpr int kUnits = kNC / 8;  // 16-byte units per row, at most
       const int unit = lane % kUnits;
 #pragma unroll
       for (int i = 0; i < kUnits; ++i) {
         const int r = i * (32 / kUnits) + lane / kUnits;
         if (row0 + r < r1 && unit * 8 < cols)
-          *reinterpret_cast<uint4*>(warp_buf + r * kPitch + unit * 16) =
-              *reinterpret_cast<const uint4*>(a.add + static_cast<int64_t>(row0 + r) * a.ldadd + col + unit * 8);
+          asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(smem_u32(lines + r * kPitch + unit * 16)),
+                       "l"(a.add + static_cast<int64_t>(row0 + r) * a.ldadd + col + unit * 8)
+                       : "memory");
       }
-      __syncwarp();
+    } else {
+      const int rows = min(32, r1 - row0);
+      for (int r = 0; r < rows; ++r)
+        for (int c = lane; c < cols; c += 32)
+          reinterpret_cast<uint16_t*>(lines + r * kPitch)[c] = a.add[static_cast<int64_t>(row0 + r) * a.ldadd + col + c];
     }
   }
 
+  // Before the first put8: the residual is there.
+  __device__ __forceinline__ void ready(const ProductArgs& a) {
+    if (!a.add) return;
+    asm volatile("cp.async.wait_all;" ::: "memory");
+    __syncwarp();
+  }
+
   __device__ __forceinline__ void put8(const ProductArgs& a, int c, float (&x)[8]) {
-    if (row >= r1) return;
-    if (!bulk) {
-      store8(a, row, col + c, x);
-      return;
-    }
-    uint4* p = reinterpret_cast<uint4*>(line + c * 2);
+    uint4* p = reinterpret_cast<uint4*>(lines + lane * kPitch + c * 2);
     if (a.add) {
       const uint4 v = *p;
       const uint32_t w[4] = {v.x, v.y, v.z, v.w};
@@ -225,14 +211,22 @@ struct RowsOut {
   }
 
   __device__ __forceinline__ void send(const ProductArgs& a) {
-    if (bulk && row < r1 && cols > 0) {
-      asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
-      asm volatile("cp.async.bulk.global.shared::cta.bulk_group [%0], [%1], %2;" ::"l"(
-                       a.Y + static_cast<int64_t>(row) * a.ldy + col),
-                   "r"(smem_u32(line)), "r"(cols * 2)
-                   : "memory");
+    if (bulk) {
+      if (row0 + lane < r1 && cols > 0) {
+        asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
+        asm volatile("cp.async.bulk.global.shared::cta.bulk_group [%0], [%1], %2;" ::"l"(
+                         a.Y + static_cast<int64_t>(row0 + lane) * a.ldy + col),
+                     "r"(smem_u32(lines + lane * kPitch)), "r"(cols * 2)
+                     : "memory");
+      }
+      asm volatile("cp.async.bulk.commit_group;" ::: "memory");
+    } else {
+      __syncwarp();
+      const int rows = min(32, r1 - row0);
+      for (int r = 0; r < rows; ++r)
+        for (int c = lane; c < cols; c += 32)
+          a.Y[static_cast<int64_t>(row0 + r) * a.ldy + col + c] = reinterpret_cast<const uint16_t*>(lines + r * kPitch)[c];
     }
-    asm volatile("cp.async.bulk.commit_group;" ::: "memory");
   }
 };
 
@@ -652,6 +646,8 @@ __global__ void __launch_bounds__(kTileThreads, 1)
       const int row0 = u.m0 + static_cast<int>(rank) * kRowTile + quarter * 32;  // the warp's 32 rows
       const int col0 = u.n0 + half * kNC;
       if constexpr (kF8) {
+        RowsOut<kNC> rows_out;
+        if (!split) rows_out.begin(args, out_buf, row0, u.r1, col0, kNC, lane);
         float acc[kNC];
 #pragma unroll
         for (int i = 0; i < kNC; ++i) acc[i] = 0.f;
@@ -709,8 +705,7 @@ __global__ void __launch_bounds__(kTileThreads, 1)
             part[c * kRowTile] = make_float4(acc[4 * c], acc[4 * c + 1], acc[4 * c + 2], acc[4 * c + 3]);
           break;
         }
-        RowsOut<kNC> rows_out;
-        rows_out.begin(args, out_buf, row0, u.r1, col0, lane);
+        rows_out.ready(args);
 #pragma unroll
         for (int c = 0; c < kNC; c += 8) {
           float x[8];
@@ -720,10 +715,11 @@ __global__ void __launch_bounds__(kTileThreads, 1)
         }
         rows_out.send(args);
       } else {
+        RowsOut<kNC> rows_out;
+        if (!split) rows_out.begin(args, out_buf, row0, u.r1, col0, kNC, lane);
         if (!wait_bar(my_tfull + 8 * C::kHalves * acc_buf, acc_phase, abort_flag, args.status, args.timeout_ns)) break;
         tc_fence_after();
-        RowsOut<kNC> rows_out;
-        if (!split) rows_out.begin(args, out_buf, row0, u.r1, col0, lane);
+        if (!split) rows_out.ready(args);
 #pragma unroll 1
         for (int g = 0; g < kNC / 32; ++g) {
           uint32_t r[32];
@@ -755,7 +751,6 @@ __global__ void __launch_bounds__(kTileThreads, 1)
         }
       }
     }
-    asm volatile("cp.async.bulk.wait_group.read 0;" ::: "memory");
     if (split) {
       // Every CTA of the cluster adds its columns of the tile over the shares, in order.
       // (The operand stages are free: the accumulator's last hand-over follows every MMA.)
@@ -765,22 +760,25 @@ __global__ void __launch_bounds__(kTileThreads, 1)
         const int per = kBN / (2 * args.split);  // columns per thread: 32, 16 or 8
         const int r = quarter * 32 + lane;
         const int c0 = static_cast<int>(cta) * 2 * per + half * per;
-        if (u.m0 + r < u.r1) {
-          for (int c = c0; c < c0 + per; c += 8) {
-            float x[8];
-            for (int k = 0; k < args.split; ++k) {
-              const uint32_t p = mapa_shared(smem_u32(smem) + ((c / 4) * kRowTile + r) * 16, k);
-              const float4 a = ld_cluster(p), b = ld_cluster(p + kRowTile * 16);
-              const float v[8] = {a.x, a.y, a.z, a.w, b.x, b.y, b.z, b.w};
+        RowsOut<kNC> rows_out;
+        rows_out.begin(args, out_buf, u.m0 + quarter * 32, u.r1, u.n0 + c0, per, lane);
+        rows_out.ready(args);
+        for (int c = 0; c < per; c += 8) {
+          float x[8];
+          for (int k = 0; k < args.split; ++k) {
+            const uint32_t p = mapa_shared(smem_u32(smem) + (((c0 + c) / 4) * kRowTile + r) * 16, k);
+            const float4 a = ld_cluster(p), b = ld_cluster(p + kRowTile * 16);
+            const float v[8] = {a.x, a.y, a.z, a.w, b.x, b.y, b.z, b.w};
 #pragma unroll
-              for (int j = 0; j < 8; ++j) x[j] = k == 0 ? v[j] : __fadd_rn(x[j], v[j]);
-            }
-            store8(args, u.m0 + r, u.n0 + c, x);
+            for (int j = 0; j < 8; ++j) x[j] = k == 0 ? v[j] : __fadd_rn(x[j], v[j]);
           }
+          rows_out.put8(args, c, x);
         }
+        rows_out.send(args);
       }
       cluster_sync_all();  // no CTA leaves while another reads its shares
     }
+    asm volatile("cp.async.wait_all;\n\tcp.async.bulk.wait_group.read 0;" ::: "memory");
   }
 
   __syncwarp();
