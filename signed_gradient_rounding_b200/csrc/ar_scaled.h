@@ -82,7 +82,7 @@ struct ProductArgs {
   int64_t ldy = 0;
   int vec_y = 0;                     // Y and add take 16-byte accesses at multiples of 8 columns
   int split = 1;                     // CTAs of a cluster that share K (set by the launch)
-  int* status = nullptr;
+  int* status = nullptr;             // null: a word of the library's
   uint64_t timeout_ns = 1000000000ull;
 };
 constexpr int kMaxExperts = 1024;

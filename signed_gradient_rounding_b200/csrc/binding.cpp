@@ -233,6 +233,7 @@ PyObject* rms_norm(PyObject*, PyObject* const* a, Py_ssize_t nargs) {
         h = tensor(a[6], "sum_out");
         lds = pitch(h, "sum_out", dev, rows, cols);
         typed(h, "sum_out", r.scalar_type());
+        if (h.data_ptr() == x.data_ptr()) throw Refused("sum_out must not be x");
       }
     } else if (!none(a[6])) {
       throw Refused("sum_out needs a residual");
@@ -380,6 +381,7 @@ PyObject* grouped_linear(PyObject*, PyObject* const* a, Py_ssize_t nargs) {
     int32_t* status = status_of(a[5], dev);
     int64_t ldy = out;
     at::Tensor Y = output(a[4], dev, n, out, &ldy);
+    if (n > 0 && Y.data_ptr() == X.data_ptr()) throw Refused("out must not be X");
     void* st = stream_of(a[6], dev);
     launch(dev, "ar_grouped_linear", [&] {
       return ar_grouped_linear(static_cast<const uint16_t*>(X.data_ptr()), ldx, n, in,

@@ -25,14 +25,6 @@ bool dtype_ok(ar_dtype t) { return t == AR_F32 || t == AR_BF16; }
 
 ar_status from_cuda(cudaError_t e) { return e == cudaSuccess ? AR_OK : AR_ECUDA; }
 
-// Where the products' bounded waits report when the caller passes no status word.
-__device__ int g_product_status;
-
-ar_status product_status(int32_t** status) {
-  if (*status) return AR_OK;
-  return from_cuda(cudaGetSymbolAddress(reinterpret_cast<void**>(status), g_product_status));
-}
-
 // The checks that the three products share.  el: bytes per operand element.
 ar_status check_product(const void* X, int64_t ldx, int64_t n, int64_t in, const void* W, int64_t ldw, int64_t experts,
                         int64_t out, const void* Y, int64_t ldy, int el) {
@@ -161,13 +153,11 @@ ar_status ar_silu_mul_scaled(const uint16_t* a, int64_t lda, const uint16_t* b, 
 ar_status ar_linear_scaled(const uint8_t* X, int64_t ldx, const float* x_scale, int64_t n, int64_t in, const uint8_t* W,
                            int64_t ldw, const float* w_scale, int64_t out, const uint16_t* add, int64_t ldadd,
                            uint16_t* Y, int64_t ldy, int32_t* status, void* stream) {
-  ar_status s = check_product(X, ldx, n, in, W, ldw, 1, out, Y, ldy, 1);
+  const ar_status s = check_product(X, ldx, n, in, W, ldw, 1, out, Y, ldy, 1);
   if (s != AR_OK || n == 0) return s;
   if (!x_scale || !w_scale || !aligned(x_scale, 4) || !aligned(w_scale, 4)) return AR_EINVAL;
   if (add && (ldadd < out || !aligned(add, 2))) return AR_EINVAL;
   if (fault_is("launch")) return AR_ECUDA;
-  s = product_status(&status);
-  if (s != AR_OK) return s;
   ar::ProductArgs a;
   a.f8 = 1;
   a.X = X;
@@ -193,12 +183,10 @@ ar_status ar_linear_scaled(const uint8_t* X, int64_t ldx, const float* x_scale, 
 ar_status ar_grouped_linear(const uint16_t* X, int64_t ldx, int64_t n, int64_t in, const int32_t* offsets,
                             int64_t experts, const uint16_t* W_hi, const uint16_t* W_lo, int64_t ldw, int64_t out,
                             uint16_t* Y, int64_t ldy, int32_t* status, void* stream) {
-  ar_status s = check_product(X, ldx, n, in, W_hi, ldw, experts, out, Y, ldy, 2);
+  const ar_status s = check_product(X, ldx, n, in, W_hi, ldw, experts, out, Y, ldy, 2);
   if (s != AR_OK || n == 0) return s;
   if (!offsets || !aligned(offsets, 4) || !aligned(W_lo, 16)) return AR_EINVAL;
   if (fault_is("launch")) return AR_ECUDA;
-  s = product_status(&status);
-  if (s != AR_OK) return s;
   ar::ProductArgs a;
   a.X = X;
   a.ldx = ldx * 2;
@@ -223,13 +211,11 @@ ar_status ar_grouped_linear_scaled(const uint8_t* X, int64_t ldx, const float* x
                                    const int32_t* offsets, int64_t experts, const uint8_t* W, int64_t ldw,
                                    const float* w_scale, int64_t out, uint16_t* Y, int64_t ldy, int32_t* status,
                                    void* stream) {
-  ar_status s = check_product(X, ldx, n, in, W, ldw, experts, out, Y, ldy, 1);
+  const ar_status s = check_product(X, ldx, n, in, W, ldw, experts, out, Y, ldy, 1);
   if (s != AR_OK || n == 0) return s;
   if (!offsets || !aligned(offsets, 4) || !x_scale || !w_scale || !aligned(x_scale, 4) || !aligned(w_scale, 4))
     return AR_EINVAL;
   if (fault_is("launch")) return AR_ECUDA;
-  s = product_status(&status);
-  if (s != AR_OK) return s;
   ar::ProductArgs a;
   a.f8 = 1;
   a.X = X;

@@ -25,6 +25,9 @@ namespace ar {
 
 namespace {
 
+// Where bounded waits report when the caller passes no status word.
+__device__ int g_product_status;
+
 // Rows [r0, r1) of X that belong to expert e, clamped to the tensor: whatever the
 // offsets hold, no access leaves it.
 __device__ __forceinline__ void expert_rows(const ProductArgs& a, int e, int& r0, int& r1) {
@@ -381,6 +384,7 @@ __global__ void __launch_bounds__(kTileThreads, 1)
   uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
   TileSmem* sm = reinterpret_cast<TileSmem*>(smem + C::kBarOffset);
   volatile int* abort_flag = &sm->abort_flag;
+  int* status = args.status ? args.status : &g_product_status;
   const int warp = __shfl_sync(0xffffffffu, static_cast<int>(threadIdx.x >> 5), 0);  // warp-uniform
   const int lane = threadIdx.x & 31;
   // A cluster is a pair of CTAs that share a 256-row tile, or args.split CTAs that share K.
@@ -479,7 +483,7 @@ __global__ void __launch_bounds__(kTileThreads, 1)
         const int x_row = u.m0 + static_cast<int>(rank) * kRowTile;
         const int w_row = u.e * args.out + u.n0 + static_cast<int>(rank) * (C::kBRows / C::kWBoxes);
         for (int kb = k_begin; kb < k_end; ++kb) {
-          if (!wait_bar(bar_empty + 8 * stage, phase ^ 1, abort_flag, args.status, args.timeout_ns)) {
+          if (!wait_bar(bar_empty + 8 * stage, phase ^ 1, abort_flag, status, args.timeout_ns)) {
             ok = false;
             break;
           }
@@ -532,8 +536,8 @@ __global__ void __launch_bounds__(kTileThreads, 1)
             // both tests in flight at once: each takes over 100 cycles, passed or not
             const bool free = !first || mbar_try_wait(bar_tempty + bar_acc, acc_phase ^ 1);
             const bool here = mbar_try_wait(bar_full + 8 * stage, phase);
-            if (!free) ok = wait_bar(bar_tempty + bar_acc, acc_phase ^ 1, abort_flag, args.status, args.timeout_ns);
-            if (ok && !here) ok = wait_bar(bar_full + 8 * stage, phase, abort_flag, args.status, args.timeout_ns);
+            if (!free) ok = wait_bar(bar_tempty + bar_acc, acc_phase ^ 1, abort_flag, status, args.timeout_ns);
+            if (ok && !here) ok = wait_bar(bar_full + 8 * stage, phase, abort_flag, status, args.timeout_ns);
             if (!ok) break;
             tc_fence_after();
             const uint32_t d_tmem = tmem_base + acc * kBN + half * C::kMmaN;
@@ -590,7 +594,7 @@ __global__ void __launch_bounds__(kTileThreads, 1)
         const int fills = scale_slots(k_end - k_begin);
         for (int j = 0; j < fills; ++j, ++slots) {
           const int slot = slots % kScaleSlots;
-          if (!wait_bar(smem_u32(&sm->sempty[slot]), (slots / kScaleSlots & 1) ^ 1, abort_flag, args.status,
+          if (!wait_bar(smem_u32(&sm->sempty[slot]), (slots / kScaleSlots & 1) ^ 1, abort_flag, status,
                         args.timeout_ns)) {
             ok = false;
             break;
@@ -659,7 +663,7 @@ __global__ void __launch_bounds__(kTileThreads, 1)
         for (int k = 0; k < blocks; ++k) {
           if (k == 0 || k % kScaleKb == 1) {  // slot (k + 3) / 4 is new to the rows that are furthest ahead
             const uint32_t j = slots + (k + kScaleKb - 1) / kScaleKb;
-            if (!wait_bar(smem_u32(&sm->sfull[j % kScaleSlots]), j / kScaleSlots & 1, abort_flag, args.status,
+            if (!wait_bar(smem_u32(&sm->sfull[j % kScaleSlots]), j / kScaleSlots & 1, abort_flag, status,
                           args.timeout_ns)) {
               ok = false;
               break;
@@ -672,7 +676,7 @@ __global__ void __launch_bounds__(kTileThreads, 1)
             __syncwarp();
             if (lane == 0) mbar_arrive(&sm->sempty[(slots + k / kScaleKb) % kScaleSlots]);
           }
-          if (!wait_bar(my_tfull + 8 * C::kHalves * acc_buf, acc_phase, abort_flag, args.status, args.timeout_ns)) {
+          if (!wait_bar(my_tfull + 8 * C::kHalves * acc_buf, acc_phase, abort_flag, status, args.timeout_ns)) {
             ok = false;
             break;
           }
@@ -717,7 +721,7 @@ __global__ void __launch_bounds__(kTileThreads, 1)
       } else {
         RowsOut<kNC> rows_out;
         if (!split) rows_out.begin(args, out_buf, row0, u.r1, col0, kNC, lane);
-        if (!wait_bar(my_tfull + 8 * C::kHalves * acc_buf, acc_phase, abort_flag, args.status, args.timeout_ns)) break;
+        if (!wait_bar(my_tfull + 8 * C::kHalves * acc_buf, acc_phase, abort_flag, status, args.timeout_ns)) break;
         tc_fence_after();
         if (!split) rows_out.ready(args);
 #pragma unroll 1

@@ -15,6 +15,10 @@ Tolerances, from the roundings alone (u = 2^-24, half a step of fp32):
     (the bound this library's other products are held to), and one fp32 operation per
     block of K and per share of K: at most (blocks + 16) u of that sum.
 """
+import os
+import subprocess
+import sys
+
 import pytest
 import torch
 
@@ -295,6 +299,16 @@ def test_linear_scaled_pitches(ar, n, out):
     assert torch.equal(stream, Y)
 
 
+@pytest.mark.parametrize("n,inn", [(3, 1040), (200, 1040), (200, 1152), (600, 144), (70, 4112)])
+def test_linear_scaled_slice_of_a_batch(ar, n, inn):
+    """Some rows of a batch: scales that start on any of the 4-byte places of a 16-byte unit."""
+    xq, xs, wq, ws = scaled_operands(ar, n + 3, inn, 264, 3)
+    for first in range(4):
+        rows = slice(first, first + n - 1)
+        Y = ar.linear_scaled(xq[rows], xs[rows], wq, ws)
+        check_product(Y, read_rows(xq[rows], xs[rows]), read_tiles(wq, ws), nblk(inn))
+
+
 COUNTS = {
     "one": [5],
     "decode": [0, 1, 0, 3, 1, 0, 0, 2, 9],
@@ -492,6 +506,52 @@ def test_graph_with_other_offsets(ar):
         assert (Y[at:] == 3).all()
 
 
+FIRST_IN_CAPTURE = """
+import torch
+import signed_gradient_rounding_b200 as ar
+x = torch.randn(300, 512, device="cuda").bfloat16()
+w = torch.randn(2, 136, 512, device="cuda").bfloat16()
+offsets = torch.tensor([0, 100, 300], dtype=torch.int32, device="cuda")
+graph = torch.cuda.CUDAGraph()
+with torch.cuda.graph(graph):
+    y, q, s, h = ar.rms_norm(x, None, want_scaled=True)
+    wq, ws = ar.quant_scaled(w, 128)
+    big = ar.grouped_linear_scaled(q, s, offsets, wq, ws)
+    one = ar.linear_scaled(q[:1], s[:1], wq[0], ws[0])
+    mid = ar.linear_scaled(q, s, wq[1], ws[1])
+    half = ar.grouped_linear(y, offsets, w)
+graph.replay()
+torch.cuda.synchronize()
+got = [t.clone() for t in (big, one, mid, half)]
+y, q, s, h = ar.rms_norm(x, None, want_scaled=True)
+want = (ar.grouped_linear_scaled(q, s, offsets, wq, ws), ar.linear_scaled(q[:1], s[:1], wq[0], ws[0]),
+        ar.linear_scaled(q, s, wq[1], ws[1]), ar.grouped_linear(y, offsets, w))
+assert all(torch.equal(a, b) for a, b in zip(got, want))
+print("captured first")
+"""
+
+
+def test_first_calls_inside_a_capture():
+    """A process whose first call of every entry point is captured."""
+    root = os.path.dirname(os.path.dirname(os.path.abspath(__file__)))
+    r = subprocess.run([sys.executable, "-c", FIRST_IN_CAPTURE], cwd=root, capture_output=True, text=True, timeout=300)
+    assert r.returncode == 0 and "captured first" in r.stdout, r.stderr[-2000:]
+
+
+@pytest.mark.parametrize("n", [40, 400])
+@pytest.mark.parametrize("offsets", [[0, 10, 5, 30], [-7, 3, 1 << 30, 20], [25, 12, 3, 0], [1 << 30] * 4, [-(1 << 31), -1, 0, 0]])
+def test_offsets_that_break_the_rules_stay_inside(ar, n, offsets):
+    """Offsets out of range or decreasing: the rows around X and Y are neither read into Y nor written."""
+    inn, out = 256, 136
+    wide_x = torch.full((n + 256, inn), float("nan"), dtype=torch.bfloat16, device="cuda")
+    wide_x[128:128 + n] = rand(1, n, inn)
+    wide_y = torch.full((n + 256, out), 3.0, dtype=torch.bfloat16, device="cuda")
+    w = rand(2, 3, out, inn, std=0.02)
+    ar.grouped_linear(wide_x[128:128 + n], torch.tensor(offsets, dtype=torch.int32, device="cuda"), w,
+                      out=wide_y[128:128 + n])
+    assert (wide_y[:128] == 3).all() and (wide_y[128 + n:] == 3).all() and torch.isfinite(wide_y).all()
+
+
 def test_two_calls_at_once(ar):
     """Calls on two streams at once do not disturb each other."""
     a, b = scaled_operands(ar, 300, 2048, 520, 1), scaled_operands(ar, 5, 2048, 520, 2)
@@ -528,7 +588,8 @@ def test_binding_refusals(ar):
         lambda: ar.grouped_linear(bf, offsets, bf), lambda: ar.grouped_linear(bf, offsets, bf[None], bf[None, :4]),
         lambda: ar.grouped_linear_scaled(xq, xs, offsets, wq[None], ws), lambda: ar.rms_norm(bf, bf[0, :128]),
         lambda: ar.rms_norm(bf, None, residual=bf[:4]), lambda: ar.rms_norm(bf, None, sum_out=bf),
-        lambda: ar.rms_norm(bf, None, residual=bf, sum_out=bf.float()), lambda: ar.rms_norm(bf.half(), None),
+        lambda: ar.rms_norm(bf, None, residual=bf, sum_out=bf.float()), lambda: ar.rms_norm(bf, None, residual=bf, sum_out=bf),
+        lambda: ar.grouped_linear(bf, offsets, bf[None].repeat(1, 32, 1), out=bf), lambda: ar.rms_norm(bf.half(), None),
         lambda: ar.quant_scaled(bf.half()), lambda: ar.silu_mul_scaled(bf, bf[:, :128]),
         lambda: ar.silu_mul_scaled(bf.float(), bf.float()), lambda: ar.quant_scaled(bf[0]),
     ]
