@@ -7,10 +7,12 @@
 #include <torch/csrc/autograd/python_variable.h>
 
 #include <ATen/cuda/EmptyTensor.h>
+#include <c10/cuda/CUDACachingAllocator.h>
 #include <c10/cuda/CUDAFunctions.h>
 #include <c10/cuda/CUDAGuard.h>
 #include <c10/cuda/CUDAStream.h>
 
+#include <initializer_list>
 #include <stdexcept>
 #include <string>
 
@@ -119,6 +121,18 @@ void* stream_of(PyObject* o, int dev) {
   if (PyErr_Occurred()) throw Raised();
   return p;
 }
+
+// The call's tensors were used on a stream of the caller's choice: their memory is not handed
+// out again before that stream is done with them.
+void used_on(PyObject* stream, void* ptr, int dev, std::initializer_list<const at::Tensor*> tensors) {
+  if (none(stream)) return;
+  const auto s = c10::cuda::getStreamFromExternal(static_cast<cudaStream_t>(ptr), static_cast<c10::DeviceIndex>(dev));
+  for (const at::Tensor* t : tensors)
+    if (t && t->defined() && t->numel() > 0)
+      c10::cuda::CUDACachingAllocator::recordStream(t->storage().data_ptr(), s);
+}
+
+const at::Tensor* maybe(PyObject* o) { return none(o) ? nullptr : &THPVariable_Unpack(o); }
 
 // Run the call with the tensors' device current; raise ArError unless it is AR_OK.
 template <class F>
@@ -258,6 +272,7 @@ PyObject* rms_norm(PyObject*, PyObject* const* a, Py_ssize_t nargs) {
                          want_q ? static_cast<uint8_t*>(q.data_ptr()) : nullptr, cols,
                          want_q ? s.data_ptr<float>() : nullptr, st);
     });
+    used_on(a[7], st, dev, {&x, maybe(a[1]), maybe(a[3]), &y, &q, &s, &h});
     return wrap_all(y, q, s, h);
   });
 }
@@ -280,6 +295,7 @@ PyObject* quant_scaled(PyObject*, PyObject* const* a, Py_ssize_t nargs) {
       return ar_quant_scaled(x.data_ptr(), xd, ldx, count, rows, cols, static_cast<int32_t>(block_rows),
                              static_cast<uint8_t*>(q.data_ptr()), cols, s.data_ptr<float>(), st);
     });
+    used_on(a[2], st, dev, {&x, &q, &s});
     return wrap_all(q, s);
   });
 }
@@ -300,6 +316,7 @@ PyObject* silu_mul_scaled(PyObject*, PyObject* const* args, Py_ssize_t nargs) {
                                 static_cast<const uint16_t*>(b.data_ptr()), ldb, rows, cols,
                                 static_cast<uint8_t*>(q.data_ptr()), cols, s.data_ptr<float>(), st);
     });
+    used_on(args[2], st, dev, {&a, &b, &q, &s});
     return wrap_all(q, s);
   });
 }
@@ -353,6 +370,7 @@ PyObject* linear_scaled(PyObject*, PyObject* const* a, Py_ssize_t nargs) {
                               static_cast<const uint16_t*>(add), ldadd, static_cast<uint16_t*>(Y.data_ptr()), ldy, status,
                               st);
     });
+    used_on(a[7], st, dev, {&X, maybe(a[1]), &W, maybe(a[3]), maybe(a[4]), &Y});
     return result(a[5], Y);
   });
 }
@@ -389,6 +407,7 @@ PyObject* grouped_linear(PyObject*, PyObject* const* a, Py_ssize_t nargs) {
                                static_cast<const uint16_t*>(W.data_ptr()), static_cast<const uint16_t*>(lo), ldw, out,
                                static_cast<uint16_t*>(Y.data_ptr()), ldy, status, st);
     });
+    used_on(a[6], st, dev, {&X, maybe(a[1]), &W, maybe(a[3]), &Y});
     return result(a[4], Y);
   });
 }
@@ -417,6 +436,7 @@ PyObject* grouped_linear_scaled(PyObject*, PyObject* const* a, Py_ssize_t nargs)
                                       static_cast<const uint8_t*>(W.data_ptr()), ldw, static_cast<const float*>(ws), out,
                                       static_cast<uint16_t*>(Y.data_ptr()), ldy, status, st);
     });
+    used_on(a[7], st, dev, {&X, maybe(a[1]), maybe(a[2]), &W, maybe(a[4]), &Y});
     return result(a[5], Y);
   });
 }

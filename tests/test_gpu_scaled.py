@@ -567,6 +567,27 @@ def test_two_calls_at_once(ar):
         assert all(torch.equal(y, want[i]) for y in got[i])
 
 
+def test_stream_argument_keeps_memory(ar):
+    """Operands and results of a call on a given stream may be dropped at once: their memory is not
+    handed out again while that stream still works on them."""
+    ops = scaled_operands(ar, 2000, 4096, 4096, 1)
+    want = ar.linear_scaled(*ops)
+    side = torch.cuda.Stream()
+    torch.cuda.synchronize()
+    results = []
+    for _ in range(6):
+        copies = [t.clone() for t in ops]
+        side.wait_stream(torch.cuda.current_stream())
+        for _ in range(3):
+            y = ar.linear_scaled(*copies, stream=side)
+        results.append(y)
+        del copies, y
+        for t in ops:  # takes the copies' memory, if it is free
+            torch.zeros_like(t, dtype=torch.uint8 if t.dtype == torch.float8_e4m3fn else t.dtype).fill_(127)
+    torch.cuda.synchronize()
+    assert all(torch.equal(y, want) for y in results)
+
+
 def test_status_word_stays_zero(ar):
     status = torch.zeros(1, dtype=torch.int32, device="cuda")
     ops = scaled_operands(ar, 300, 1024, 520, 1)
