@@ -304,6 +304,12 @@ __device__ __forceinline__ void tma_load_if(uint32_t leader, uint32_t dst, const
         : "memory");
 }
 
+__device__ __forceinline__ float ld_shared(uint32_t addr) {
+  float v;
+  asm volatile("ld.shared.f32 %0, [%1];" : "=f"(v) : "r"(addr) : "memory");
+  return v;
+}
+
 __device__ __forceinline__ float4 ld_cluster(uint32_t addr) {
   float4 v;
   asm volatile("ld.shared::cluster.v4.f32 {%0, %1, %2, %3}, [%4];"
@@ -636,9 +642,9 @@ __global__ void __launch_bounds__(kTileThreads, 1)
     const uint32_t my_tfull = bar_tfull + (C::kHalves == 2 ? 8 * half : 0);
     const uint32_t my_tempty =
         (kPair ? mapa_shared(bar_tempty, 0) : bar_tempty) + (C::kHalves == 2 ? 8 * half : 0);
-    auto release = [&](int buf) {
+    const uint32_t xs_base = smem_u32(sm->xs[0][quarter * 32 + lane]), ws_base = smem_u32(&sm->ws[0][0][half]);
+    auto release = [&](int buf) {  // (tcgen05.wait::ld, before it, is the whole warp's)
       tc_fence_before();
-      __syncwarp();
       if (lane == 0) mbar_arrive_remote(my_tempty + 8 * C::kHalves * buf);
     };
     int acc_buf = 0;
@@ -656,22 +662,27 @@ __global__ void __launch_bounds__(kTileThreads, 1)
 #pragma unroll
         for (int i = 0; i < kNC; ++i) acc[i] = 0.f;
         // The row's scales start `skew` into its 16-byte pieces: block k is in slot (skew + k) / 4.
+        // Byte offsets that move with k, and 64 columns in flight: 876 -> 867 us at n = 16384, 4096 -> 11008.
         const int blocks = k_end - k_begin;
-        const int skew =
-            (static_cast<uint32_t>(row0 + lane) * static_cast<uint32_t>(nkb) + k_begin) % kScaleKb;
+        const uint32_t skew = (static_cast<uint32_t>(row0 + lane) * static_cast<uint32_t>(nkb) + k_begin) % kScaleKb;
+        constexpr uint32_t kSlotBytes = kRowTile * kScaleKb * 4;
+        uint32_t x_off = slots % kScaleSlots * kSlotBytes + skew * 4;
+        uint32_t w_off = slots % kScaleSlots * (kScaleKb * 8);
+        uint32_t next_slot = slots;  // to wait for
 #pragma unroll 1
         for (int k = 0; k < blocks; ++k) {
-          if (k == 0 || k % kScaleKb == 1) {  // slot (k + 3) / 4 is new to the rows that are furthest ahead
-            const uint32_t j = slots + (k + kScaleKb - 1) / kScaleKb;
-            if (!wait_bar(smem_u32(&sm->sfull[j % kScaleSlots]), j / kScaleSlots & 1, abort_flag, status,
+          if (k == 0 || k % kScaleKb == 1) {  // a slot that is new to the rows that are furthest ahead
+            if (!wait_bar(smem_u32(&sm->sfull[next_slot % kScaleSlots]), next_slot / kScaleSlots & 1, abort_flag, status,
                           args.timeout_ns)) {
               ok = false;
               break;
             }
+            ++next_slot;
           }
-          const float s = __fmul_rn(
-              sm->xs[(slots + (skew + k) / kScaleKb) % kScaleSlots][quarter * 32 + lane][(skew + k) % kScaleKb],
-              sm->ws[(slots + k / kScaleKb) % kScaleSlots][k % kScaleKb][half]);
+          const float s = __fmul_rn(ld_shared(xs_base + x_off), ld_shared(ws_base + w_off));
+          x_off += 4;
+          if ((x_off & 15) == 0) x_off = (x_off + kSlotBytes - 16) % (kScaleSlots * kSlotBytes);
+          w_off = (w_off + 8) % (kScaleSlots * kScaleKb * 8);
           if (k % kScaleKb == kScaleKb - 1) {  // no row needs slot k / 4 any more
             __syncwarp();
             if (lane == 0) mbar_arrive(&sm->sempty[(slots + k / kScaleKb) % kScaleSlots]);
@@ -682,13 +693,16 @@ __global__ void __launch_bounds__(kTileThreads, 1)
           }
           tc_fence_after();
 #pragma unroll
-          for (int g = 0; g < kNC / 32; ++g) {
-            uint32_t r[32];
-            tmem_ld_32cols(t_lane + acc_buf * kBN + g * 32, r);
+          for (int g = 0; g < kNC / 64; ++g) {
+            uint32_t r[32], q[32];
+            tmem_ld_32cols(t_lane + acc_buf * kBN + g * 64, r);
+            tmem_ld_32cols(t_lane + acc_buf * kBN + g * 64 + 32, q);
             tmem_ld_wait();
-            if (g == kNC / 32 - 1) release(acc_buf);
+            if (g == kNC / 64 - 1) release(acc_buf);
 #pragma unroll
-            for (int j = 0; j < 32; ++j) acc[g * 32 + j] = fmaf(__uint_as_float(r[j]), s, acc[g * 32 + j]);
+            for (int j = 0; j < 32; ++j) acc[g * 64 + j] = fmaf(__uint_as_float(r[j]), s, acc[g * 64 + j]);
+#pragma unroll
+            for (int j = 0; j < 32; ++j) acc[g * 64 + 32 + j] = fmaf(__uint_as_float(q[j]), s, acc[g * 64 + 32 + j]);
           }
           if (++acc_buf == C::kAccs) {
             acc_buf = 0;
