@@ -56,6 +56,35 @@ struct TileQuantArgs {
   float* scale = nullptr;  // [count, row_blocks, blocks]
 };
 
+// Launches of the chain overlap their own start with the end of the launch before them
+// (programmatic dependent launch): a kernel lets the next one start as soon as all of its
+// own blocks have (chain_next), and waits for the one before it to complete, its writes
+// visible, before it touches memory (chain_wait, by every thread of every block, first of
+// all).  A launch without the attribute before or after it is ordered as ever.
+#ifdef __CUDACC__
+__device__ __forceinline__ void chain_next() { asm volatile("griddepcontrol.launch_dependents;" ::: "memory"); }
+__device__ __forceinline__ void chain_wait() { asm volatile("griddepcontrol.wait;" ::: "memory"); }
+
+template <class... P, class... A>
+cudaError_t launch_chained(void (*fn)(P...), dim3 grid, dim3 block, size_t smem, int cluster, cudaStream_t st, A&&... args) {
+  cudaLaunchAttribute attr[2];
+  attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attr[0].val.programmaticStreamSerializationAllowed = 1;
+  attr[1].id = cudaLaunchAttributeClusterDimension;
+  attr[1].val.clusterDim.x = static_cast<unsigned>(cluster);
+  attr[1].val.clusterDim.y = 1;
+  attr[1].val.clusterDim.z = 1;
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = grid;
+  cfg.blockDim = block;
+  cfg.dynamicSmemBytes = smem;
+  cfg.stream = st;
+  cfg.attrs = attr;
+  cfg.numAttrs = cluster > 1 ? 2 : 1;
+  return cudaLaunchKernelEx(&cfg, fn, static_cast<P>(args)...);
+}
+#endif
+
 cudaError_t launch_rms_norm(const RmsNormArgs& a, cudaStream_t st);
 cudaError_t launch_row_quant(const RowQuantArgs& a, cudaStream_t st);
 cudaError_t launch_tile_quant(const TileQuantArgs& a, cudaStream_t st);

@@ -398,6 +398,7 @@ __global__ void __launch_bounds__(kTileThreads, 1)
   const uint32_t cta = kPair || split ? cluster_ctarank() : 0u;
   const uint32_t rank = kPair ? cta : 0u;
 
+  chain_next();
   if (warp == 1 && lane == 0) {
     for (int s = 0; s < C::kStages; ++s) {
       mbar_init(&sm->full[s], 1);
@@ -430,6 +431,7 @@ __global__ void __launch_bounds__(kTileThreads, 1)
       if (args.W_lo) tma_prefetch_desc(&tmWlo);
     }
   }
+  chain_wait();  // (barriers and tensor memory, above, are this block's own)
   if (warp == 2) {
     // Row blocks before each expert.  Capped at what monotone offsets can give, so
     // that no offsets overflow the count.
@@ -893,6 +895,8 @@ __global__ void __launch_bounds__(32 * kSkinnyWarps) skinny_kernel(const __grid_
   using C = SkinnyCfg<kF8, kNT, kMR, kS>;
   constexpr int kTok = C::kTok, kRows = C::kRows;
   extern __shared__ uint4 skinny_smem[];
+  chain_next();
+  chain_wait();
   const int e = blockIdx.y;
   int r0, r1;
   expert_rows(a, e, r0, r1);
@@ -1074,8 +1078,7 @@ cudaError_t launch_skinny(const ProductArgs& a, const DeviceInfo& d, cudaStream_
     ready[d.dev].store(1, std::memory_order_relaxed);
   }
   const dim3 grid((a.out + C::kRows - 1) / C::kRows, a.experts);
-  fn<<<grid, 32 * kSkinnyWarps, C::kSmemBytes, st>>>(a);
-  return cudaGetLastError();
+  return launch_chained(fn, grid, dim3(32 * kSkinnyWarps), C::kSmemBytes, 1, st, a);
 }
 
 // Units of bm rows x bn columns that can have work (exact for one expert).
@@ -1090,24 +1093,23 @@ cudaError_t launch_tile(ProductArgs a, const DeviceInfo& d, cudaStream_t st, int
   // Per kernel and device: the resident units (CTAs or pairs), once its
   // shared-memory limit is raised.  0: not yet done.
   static std::atomic<int> resident[64];
-  cudaLaunchConfig_t cfg = {};
-  cfg.blockDim = dim3(kTileThreads);
-  cfg.dynamicSmemBytes = C::kSmemBytes;
-  cfg.stream = st;
-  cudaLaunchAttribute attr[1];
-  attr[0].id = cudaLaunchAttributeClusterDimension;
-  attr[0].val.clusterDim.x = kPair ? 2 : 1;
-  attr[0].val.clusterDim.y = 1;
-  attr[0].val.clusterDim.z = 1;
-  cfg.attrs = attr;
-  cfg.numAttrs = 1;
   int units = resident[d.dev].load(std::memory_order_relaxed);
   if (units == 0) {
     cudaError_t e = cudaFuncSetAttribute(fn, cudaFuncAttributeMaxDynamicSharedMemorySize, C::kSmemBytes);
     if (e != cudaSuccess) return e;
     units = d.sms;
     if (kPair) {
+      cudaLaunchAttribute attr[1];
+      attr[0].id = cudaLaunchAttributeClusterDimension;
+      attr[0].val.clusterDim.x = 2;
+      attr[0].val.clusterDim.y = 1;
+      attr[0].val.clusterDim.z = 1;
+      cudaLaunchConfig_t cfg = {};
       cfg.gridDim = dim3(2 * (d.sms / 2));
+      cfg.blockDim = dim3(kTileThreads);
+      cfg.dynamicSmemBytes = C::kSmemBytes;
+      cfg.attrs = attr;
+      cfg.numAttrs = 1;
       e = cudaOccupancyMaxActiveClusters(&units, fn, &cfg);
       if (e != cudaSuccess) return e;
       units = units < d.sms / 2 ? units : d.sms / 2;
@@ -1130,9 +1132,8 @@ cudaError_t launch_tile(ProductArgs a, const DeviceInfo& d, cudaStream_t st, int
   if (a.W_lo) e = make_tmap_bytes(&mlo, a.W_lo, w_rows, bytes, a.ldw, C::kBRows / C::kWBoxes);
   if (e != cudaSuccess) return e;
   const int cluster = kPair ? 2 : split;
-  attr[0].val.clusterDim.x = cluster;
-  cfg.gridDim = dim3(static_cast<unsigned>(cluster * units));
-  return cudaLaunchKernelEx(&cfg, fn, mx, mw, mlo, a);
+  return launch_chained(fn, dim3(static_cast<unsigned>(cluster * units)), dim3(kTileThreads), C::kSmemBytes, cluster, st,
+                        mx, mw, mlo, a);
 }
 
 // Which kernel.  Both operand types, times on one B200 in us (e4m3 unless said).

@@ -274,6 +274,8 @@ __global__ void __launch_bounds__(kOcts == 2 ? 704 : 1024, kOcts == 2 ? 2 : 1) r
   using XT = typename OctOf<kXBf16, kVec>::type;
   using RT = typename OctOf<kRes == 2, kVec>::type;
   __shared__ float partial[32];
+  chain_next();
+  chain_wait();
   const int64_t row = static_cast<int64_t>(blockIdx.x) * blockDim.y + threadIdx.y;
   if (row >= a.rows) return;  // whole warps (blockDim.y > 1 only for one-warp teams)
   const int cols = a.cols;
@@ -386,10 +388,9 @@ __global__ void __launch_bounds__(kOcts == 2 ? 704 : 1024, kOcts == 2 ? 2 : 1) r
 template <bool kXBf16, int kRes, int kOcts>
 cudaError_t launch_norm_octs(const RmsNormArgs& a, bool vec, dim3 grid, dim3 block, cudaStream_t st) {
   if (vec)
-    rms_norm_kernel<kXBf16, kRes, kOcts, true><<<grid, block, 0, st>>>(a);
+    return launch_chained(rms_norm_kernel<kXBf16, kRes, kOcts, true>, grid, block, 0, 1, st, a);
   else
-    rms_norm_kernel<kXBf16, kRes, kOcts, false><<<grid, block, 0, st>>>(a);
-  return cudaGetLastError();
+    return launch_chained(rms_norm_kernel<kXBf16, kRes, kOcts, false>, grid, block, 0, 1, st, a);
 }
 
 template <bool kXBf16, int kRes>
@@ -403,6 +404,10 @@ cudaError_t launch_norm(RmsNormArgs a, bool vec, cudaStream_t st) {
     if (octs <= 64) return launch_norm_octs<kXBf16, kRes, 2>(a, vec, grid, block, st);
     return launch_norm_octs<kXBf16, kRes, 4>(a, vec, grid, block, st);
   }
+  // A CTA per row.  Two octs a thread from 512 of them (given rows for two CTAs an SM or more) up to
+  // what two CTAs of 704 threads hold; four above.  (5000 x 11008 with a bf16 residual: 119 us with
+  // one CTA an SM, 76 with two.  A pair of CTAs per row above, to have two rows an
+  // SM there too, was no faster: 2000 x 29568 103 us for 95.)
   const dim3 grid(static_cast<unsigned>(a.rows));
   const int per = octs <= 1024 ? (octs <= 512 && a.rows > 296 ? 2 : 1) : octs <= 1408 ? 2 : 4;
   const dim3 block(static_cast<unsigned>(((octs + per - 1) / per + 31) / 32 * 32));
@@ -439,6 +444,8 @@ template <bool kXBf16, bool kGated, bool kVec>
 __global__ void __launch_bounds__(256, kVec ? 4 : 1) row_quant_kernel(RowQuantArgs a) {
   using XT = typename OctOf<kXBf16, kVec>::type;
   constexpr int kUnits = kUnitsOf<kVec>;
+  chain_next();
+  chain_wait();
   // Unit u is block u % blocks of row u / blocks.  A warp takes 2 kUnits consecutive units;
   // step i of its lanes: kVec, unit first + i of its half; else units first + 2 i and + 2 i + 1.
   const int64_t warp = (static_cast<int64_t>(blockIdx.x) * blockDim.x + threadIdx.x) >> 5;
@@ -521,6 +528,8 @@ template <bool kXBf16, bool kVec>
 __global__ void __launch_bounds__(512, 2) tile_quant_kernel(TileQuantArgs a) {
   using XT = typename OctOf<kXBf16, kVec>::type;
   __shared__ float partial[16];
+  chain_next();
+  chain_wait();
   const int64_t tile = blockIdx.x;
   const int64_t per_mat = static_cast<int64_t>(a.row_blocks) * a.blocks;
   const int64_t mat = tile / per_mat;
@@ -577,6 +586,8 @@ __global__ void __launch_bounds__(512, 2) tile_quant_kernel(TileQuantArgs a) {
 __global__ void __launch_bounds__(256, 6) tile_quant_async_kernel(TileQuantArgs a) {
   __shared__ uint4 buf[8 * 256];
   __shared__ float partial[8];
+  chain_next();
+  chain_wait();
   const int64_t tile = blockIdx.x;
   const int64_t per_mat = static_cast<int64_t>(a.row_blocks) * a.blocks;
   const int64_t mat = tile / per_mat;
@@ -648,21 +659,17 @@ cudaError_t launch_row_quant(const RowQuantArgs& a, cudaStream_t st) {
   const int per_warp = 2 * (vec ? kUnitsOf<true> : kUnitsOf<false>);
   const int64_t warps = (a.rows * a.blocks + per_warp - 1) / per_warp;
   const unsigned grid = static_cast<unsigned>((warps + 7) / 8);
-#define AR_ROW_QUANT(BF, GATED)                                   \
-  do {                                                            \
-    if (vec)                                                      \
-      row_quant_kernel<BF, GATED, true><<<grid, 256, 0, st>>>(a);  \
-    else                                                          \
-      row_quant_kernel<BF, GATED, false><<<grid, 256, 0, st>>>(a); \
-  } while (0)
-  if (a.gate)
-    AR_ROW_QUANT(true, true);
-  else if (a.x_bf16)
-    AR_ROW_QUANT(true, false);
-  else
-    AR_ROW_QUANT(false, false);
-#undef AR_ROW_QUANT
-  return cudaGetLastError();
+  const dim3 block(256);
+  if (a.gate) {
+    if (vec) return launch_chained(row_quant_kernel<true, true, true>, grid, block, 0, 1, st, a);
+    return launch_chained(row_quant_kernel<true, true, false>, grid, block, 0, 1, st, a);
+  }
+  if (a.x_bf16) {
+    if (vec) return launch_chained(row_quant_kernel<true, false, true>, grid, block, 0, 1, st, a);
+    return launch_chained(row_quant_kernel<true, false, false>, grid, block, 0, 1, st, a);
+  }
+  if (vec) return launch_chained(row_quant_kernel<false, false, true>, grid, block, 0, 1, st, a);
+  return launch_chained(row_quant_kernel<false, false, false>, grid, block, 0, 1, st, a);
 }
 
 cudaError_t launch_tile_quant(const TileQuantArgs& a, cudaStream_t st) {
@@ -670,17 +677,11 @@ cudaError_t launch_tile_quant(const TileQuantArgs& a, cudaStream_t st) {
                    a.ldq % 8 == 0;
   const unsigned grid = static_cast<unsigned>(a.count * a.row_blocks * a.blocks);
   if (a.x_bf16) {
-    if (vec)
-      tile_quant_async_kernel<<<grid, 256, 0, st>>>(a);
-    else
-      tile_quant_kernel<true, false><<<grid, 512, 0, st>>>(a);
-  } else {
-    if (vec)
-      tile_quant_kernel<false, true><<<grid, 512, 0, st>>>(a);
-    else
-      tile_quant_kernel<false, false><<<grid, 512, 0, st>>>(a);
+    if (vec) return launch_chained(tile_quant_async_kernel, grid, dim3(256), 0, 1, st, a);
+    return launch_chained(tile_quant_kernel<true, false>, grid, dim3(512), 0, 1, st, a);
   }
-  return cudaGetLastError();
+  if (vec) return launch_chained(tile_quant_kernel<false, true>, grid, dim3(512), 0, 1, st, a);
+  return launch_chained(tile_quant_kernel<false, false>, grid, dim3(512), 0, 1, st, a);
 }
 
 }  // namespace ar

@@ -203,7 +203,8 @@ def check_norm(ar, x, r, w, eps, inplace=False):
 
 
 @pytest.mark.parametrize("rows,cols", [(1, 1), (1, 128), (2, 100), (9, 256), (3, 257), (5, 1024), (4, 1032), (1, 4096), (300, 4096),
-                                       (2, 8192), (3, 8200), (2, 11008), (2, 16384), (2, 29568), (1, 32768), (2, 32767)])
+                                       (2, 8192), (3, 8200), (2, 11008), (2, 11264), (3, 11272), (2, 16384), (2, 29568), (1, 32768),
+                                       (2, 32767), (500, 12000)])
 @pytest.mark.parametrize("res", [None, torch.bfloat16, torch.float32])
 @pytest.mark.parametrize("xt", [torch.bfloat16, torch.float32])
 def test_rms_norm(ar, rows, cols, res, xt):
@@ -484,6 +485,67 @@ def test_layer_captured_and_on_another_stream(ar):
     rb.copy_(r2)
     graph.replay()
     assert torch.equal(out, want2)
+
+
+def test_launches_in_a_row_are_ordered(ar):
+    """Layers back to back, each over the buffers of the one before: as with a synchronisation between
+    them, in a stream and in a graph (the launches overlap their starts)."""
+    counts = [300, 0, 17, 99]
+    w = layer_weights(ar, 512, 256, counts)
+    xs, rs = [rand(i, sum(counts), 512) for i in range(6)], [rand(9 + i, sum(counts), 512) for i in range(6)]
+    want = []
+    for x, r in zip(xs, rs):
+        torch.cuda.synchronize()
+        want.append(layer(ar, x, r, w)[0])
+    torch.cuda.synchronize()
+    xb, rb = torch.empty_like(xs[0]), torch.empty_like(rs[0])
+
+    def chain():
+        out = []
+        for x, r in zip(xs, rs):
+            xb.copy_(x)
+            rb.copy_(r)
+            out.append(layer(ar, xb, rb, w)[0])
+        return out
+
+    for _ in range(20):
+        assert all(torch.equal(a, b) for a, b in zip(chain(), want))
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        out = chain()
+    for _ in range(10):
+        for y in out:
+            y.zero_()
+        graph.replay()
+        assert all(torch.equal(a, b) for a, b in zip(out, want))
+
+
+def test_launches_on_a_forked_stream_in_a_graph(ar):
+    """A captured launch whose result two streams read, joined again: the overlapped starts keep both orders."""
+    x, w = rand(3, 64, 512), rand(4, 512)
+    want_v = ar.rms_norm(x, w)[0]
+    want_q = ar.quant_scaled(want_v)[0]
+    want_z = ar.rms_norm(want_v, w)[0]
+    side = torch.cuda.Stream()
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        v = ar.rms_norm(x, w)[0]
+        here = torch.cuda.current_stream()
+        side.wait_stream(here)
+        with torch.cuda.stream(side):
+            q = ar.quant_scaled(v)[0]
+        z = ar.rms_norm(v, w)[0]
+        here.wait_stream(side)
+        last = ar.quant_scaled(z)[0]
+    for _ in range(5):
+        for t in (v, z):
+            t.zero_()
+        q.view(torch.uint8).zero_()
+        last.view(torch.uint8).zero_()
+        graph.replay()
+        assert torch.equal(v, want_v) and torch.equal(z, want_z)
+        assert torch.equal(q.view(torch.uint8), want_q.view(torch.uint8))
+        assert torch.equal(last.view(torch.uint8), ar.quant_scaled(want_z)[0].view(torch.uint8))
 
 
 def test_graph_with_other_offsets(ar):
