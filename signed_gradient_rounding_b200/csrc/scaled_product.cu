@@ -900,6 +900,7 @@ __global__ void __launch_bounds__(32 * kSkinnyWarps) skinny_kernel(const __grid_
   const int e = blockIdx.y;
   int r0, r1;
   expert_rows(a, e, r0, r1);
+  r0 += blockIdx.z * kTok;  // passes blockIdx.z, + gridDim.z, ...
   if (r0 >= r1) return;
   const int o0 = blockIdx.x * kRows;
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
@@ -913,7 +914,7 @@ __global__ void __launch_bounds__(32 * kSkinnyWarps) skinny_kernel(const __grid_
   uint4* ring = skinny_smem + warp * (kS * C::kPieces * 32) + lane;
   auto red = reinterpret_cast<float(*)[kTok][kRows + 1]>(skinny_smem);
 
-  for (int t0 = r0; t0 < r1; t0 += kTok) {
+  for (int t0 = r0; t0 < r1; t0 += gridDim.z * kTok) {
     float acc[kMR][kNT][4];
 #pragma unroll
     for (int m = 0; m < kMR; ++m)
@@ -1077,7 +1078,13 @@ cudaError_t launch_skinny(const ProductArgs& a, const DeviceInfo& d, cudaStream_
     if (e != cudaSuccess) return e;
     ready[d.dev].store(1, std::memory_order_relaxed);
   }
-  const dim3 grid((a.out + C::kRows - 1) / C::kRows, a.experts);
+  // The passes over X side by side while there are few CTAs (up to 8 an SM): one whose expert has no such
+  // rows leaves at once.
+  const int strips = (a.out + C::kRows - 1) / C::kRows;
+  const int64_t passes = (static_cast<int64_t>(a.n) + C::kTok - 1) / C::kTok;
+  const int64_t room = 8 * d.sms / (static_cast<int64_t>(strips) * a.experts);
+  const int64_t z = passes < room ? passes : room;
+  const dim3 grid(strips, a.experts, static_cast<unsigned>(z > 1 ? z : 1));
   return launch_chained(fn, grid, dim3(32 * kSkinnyWarps), C::kSmemBytes, 1, st, a);
 }
 
@@ -1142,8 +1149,7 @@ cudaError_t launch_tile(ProductArgs a, const DeviceInfo& d, cudaStream_t st, int
 // fixed cost but walks W again for every kTok rows; the tile one starts at 8 us (tensor
 // memory, barriers, descriptors, the first loads) and then takes 128 rows for the price of one.
 //   n = 8,  29568 -> 8192: skinny 43, tile 62         n = 16, 29568 -> 8192: skinny 48, tile 50
-//   n = 32, 4096 -> 4096:  skinny 10, tile 11.2       n = 32, 29568 -> 8192: skinny 87, tile 49
-//   n = 32, 4096 -> 11008: skinny 21, tile 18         n = 64, 4096 -> 4096:  skinny 17, tile 12
+//   n = 32, 29568 -> 8192: skinny 87, tile 49         n = 32, 4096 -> 11008: skinny 21, tile 18
 // Several experts are taken to be uneven (some have several times the average):
 //   64 experts, 4096 -> 2048, 4 rows each: 83 and 115; 8: 102 and 107; 12: 117 and 108
 //   the same in bf16, 8 rows each: 187 and 183; 12: 220 and 184
@@ -1165,9 +1171,13 @@ cudaError_t launch_type(const ProductArgs& a, const DeviceInfo& d, cudaStream_t 
   const bool one = a.experts == 1;
   if (per <= (one ? 8 : 4)) return launch_skinny<kF8, 1, 2, 2>(a, d, st);
   if (per <= (one ? 16 : 8)) return launch_skinny<kF8, 2, 2, 2>(a, d, st);
-  if (one && per <= 64 && (per + 31) / 32 * strips * a.nkb <= 8192) return launch_skinny<kF8, 4, 1, 2>(a, d, st);
-  // Row blocks: exact for one expert, else half a block more per expert, and one at least.
+  // Small products of more rows, 32 a pass and the passes side by side: the work in blocks of 16 x 32 x 128
+  // bytes.  Times of the two kernels: 64 rows, 1024 -> 1000: 3.8 and 9.3; 32, 4096 -> 4096: 9.7 and 13.6;
+  // 1000, 256 -> 512: 9.8 and 8.7 (the rule's edge); 8 experts, 96 rows in all, 1024 -> 1024: 7.7 and 11.3.
   const int64_t active = a.experts < a.n ? a.experts : a.n;
+  const int64_t passes = one ? (per + 31) / 32 : a.n / 32 + active;
+  if (passes * strips * a.nkb <= 8192) return launch_skinny<kF8, 4, 1, 2>(a, d, st);
+  // Row blocks: exact for one expert, else half a block more per expert, and one at least.
   auto waves = [&](int bm, int bn, int resident) {
     const int64_t cols = (a.out + bn - 1) / bn;
     if (a.experts == 1) return static_cast<double>(((a.n + bm - 1) / bm * cols + resident - 1) / resident);
