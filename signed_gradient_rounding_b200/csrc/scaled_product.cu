@@ -16,6 +16,7 @@
 //   * skinny_kernel: few rows per expert, bound by the weight's bytes; each weight
 //     byte goes from HBM straight into the registers of the warp that multiplies it.
 #include <atomic>
+#include <type_traits>
 
 #include "ar_device.cuh"
 #include "ar_internal.h"
@@ -96,7 +97,8 @@ struct TileCfg {
   static_assert(kBarOffset % 16 == 0 && offsetof(TileSmem, xs) % 16 == 0, "16-byte asynchronous copies");
   static_assert(kAccs * kHalves <= 4, "accumulator barriers");
   // the shares of a split K, 128 x 128 fp32, pass through the operand stages
-  static_assert(kBN != 128 || kStages * kStageBytes >= 128 * 128 * 4, "split-K exchange");
+  static constexpr bool kCanSplit = !kPair && kBN == 128;
+  static_assert(!kCanSplit || kStages * kStageBytes >= 128 * 128 * 4, "split-K exchange");
 };
 
 struct Unit {
@@ -143,23 +145,61 @@ __device__ __forceinline__ uint32_t pack2(float lo, float hi) {
   return *reinterpret_cast<const uint32_t*>(&h);
 }
 
+// 16 bytes from byte `off` (even, below 16) of the 32 bytes a, b.
+__device__ __forceinline__ uint4 bytes_at(uint4 a, uint4 b, int off) {
+  uint32_t w[8] = {a.x, a.y, a.z, a.w, b.x, b.y, b.z, b.w};
+#pragma unroll
+  for (int j = 0; j < 6; ++j) w[j] = off & 8 ? w[j + 2] : w[j];
+#pragma unroll
+  for (int j = 0; j < 5; ++j) w[j] = off & 4 ? w[j + 1] : w[j];
+#pragma unroll
+  for (int j = 0; j < 4; ++j) w[j] = __funnelshift_r(w[j], w[j + 1], off & 2 ? 16 : 0);
+  return make_uint4(w[0], w[1], w[2], w[3]);
+}
+
+// 2, 4 or 8 bytes at an address that is a multiple of as many.
+template <int kBytes>
+__device__ __forceinline__ uint2 read_piece(const uint8_t* p) {
+  if constexpr (kBytes == 8) return *reinterpret_cast<const uint2*>(p);
+  if constexpr (kBytes == 4) return make_uint2(*reinterpret_cast<const uint32_t*>(p), 0);
+  return make_uint2(*reinterpret_cast<const uint16_t*>(p), 0);
+}
+template <int kBytes>
+__device__ __forceinline__ void write_piece(uint8_t* p, uint2 v) {
+  if constexpr (kBytes == 8)
+    *reinterpret_cast<uint2*>(p) = v;
+  else if constexpr (kBytes == 4)
+    *reinterpret_cast<uint32_t*>(p) = v.x;
+  else
+    *reinterpret_cast<uint16_t*>(p) = static_cast<uint16_t>(v.x);
+}
+
 // The way out of a warp's 32 rows x up to kNC columns (lane = row; rows from r1 on belong to
 // others): each lane rounds its row's values into its own line of shared memory (put8), and
-// the lines go to Y (send): each by one bulk copy, which runs while the warp goes on with the
-// next unit, or, where Y's rows are not 16-byte aligned, by the whole warp element by
-// element.  The residual comes the same way back, asked for at the unit's start (begin).
+// the lines go to Y (send), each by one bulk copy, which runs while the warp goes on with the
+// next unit.  The residual comes the same way back, asked for at the unit's start (begin).
 // (Stored from registers, 16 bytes of 32 rows per instruction, the columns of a 256 x 256 tile
 // kept the warps for 7500 cycles; through shared memory with coalesced stores for 3700, since
-// every SM writes at the same time.  Element by element from registers, 667 rows of 944 -> 3689
-// took 54 us.)
-template <int kNC>
+// every SM writes at the same time.)
+//
+// Where rows or widths are not multiples of 16 bytes, a line is brought as far from a 16-byte
+// boundary as its row in memory is, so that the whole units of the row still leave by one bulk copy (and
+// come, for the residual, by 16-byte copies); the up to 7 elements before and after them are moved
+// in pieces of 2, 4 and 8 bytes.  A kernel of its own (not kWhole): within the other one's, that code
+// took registers from its loop over K (76 rows, 4096 -> 11008: 21.8 us for 19.2).  (All elements one by one, by the whole warp: 4574 rows, 608 -> 2785: 36 us, 26 so, 20 with
+// aligned rows.)
+template <int kNC, bool kWhole>
 struct RowsOut {
   static constexpr int kPitch = kNC * 2 + 16;
   uint8_t* lines;    // the warp's lines
   int row0, r1, col; // first row, end of the rows that exist, first column
   int cols;          // columns that exist (0 or fewer: none)
   int lane;
-  bool bulk;         // whole 16-byte units at aligned addresses
+
+  __device__ __forceinline__ const uint16_t* add_row(const ProductArgs& a, int r) const {
+    return a.add + static_cast<int64_t>(row0 + r) * a.ldadd + col;
+  }
+  static __device__ __forceinline__ int off16(const void* p) { return static_cast<int>(reinterpret_cast<uintptr_t>(p) & 15); }
 
   __device__ __forceinline__ void begin(const ProductArgs& a, uint8_t* warp_lines, int row0_, int r1_, int col_,
                                         int width, int lane_) {
@@ -169,36 +209,76 @@ struct RowsOut {
     col = col_;
     lane = lane_;
     cols = min(width, a.out - col);
-    bulk = a.vec_y && cols % 8 == 0;
     asm volatile("cp.async.bulk.wait_group.read 0;" ::: "memory");  // the last unit's copies have read the lines
     __syncwarp();  // (every lane's: the residual is brought in by the whole warp)
     if (!a.add) return;
-    if (bulk) {
-      constexpr int kUnits = kNC / 8;  // 16-byte units per row, at most
-      const int unit = lane % kUnits;
+    constexpr int kUnits = kNC / 8;  // 16-byte units per row, at most
+    const int unit = lane % kUnits;
 #pragma unroll
-      for (int i = 0; i < kUnits; ++i) {
-        const int r = i * (32 / kUnits) + lane / kUnits;
-        if (row0 + r < r1 && unit * 8 < cols)
-          asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(smem_u32(lines + r * kPitch + unit * 16)),
-                       "l"(a.add + static_cast<int64_t>(row0 + r) * a.ldadd + col + unit * 8)
-                       : "memory");
-      }
-    } else {
-      const int rows = min(32, r1 - row0);
-      for (int r = 0; r < rows; ++r)
-        for (int c = lane; c < cols; c += 32)
-          reinterpret_cast<uint16_t*>(lines + r * kPitch)[c] = a.add[static_cast<int64_t>(row0 + r) * a.ldadd + col + c];
+    for (int i = 0; i < kUnits; ++i) {
+      const int r = i * (32 / kUnits) + lane / kUnits;
+      if (row0 + r >= r1 || cols <= 0) continue;
+      const uint16_t* from = add_row(a, r);
+      const int off = kWhole ? 0 : off16(from);
+      if (unit >= (off != 0) && unit < (off + cols * 2) / 16)
+        asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(smem_u32(lines + r * kPitch + unit * 16)),
+                     "l"(reinterpret_cast<const uint8_t*>(from) - off + unit * 16)
+                     : "memory");
+    }
+    if (!kWhole && row0 + lane < r1 && cols > 0) {
+      const uint16_t* from = add_row(a, lane);
+      const int off = off16(from);
+      const uint8_t* unit0 = reinterpret_cast<const uint8_t*>(from) - off;
+      uint2 v[12];
+      edges(off, [&](auto j, auto size, int b) { v[decltype(j)::value] = read_piece<decltype(size)::value>(unit0 + b); });
+      edges(off, [&](auto j, auto size, int b) { write_piece<decltype(size)::value>(lines + lane * kPitch + b, v[decltype(j)::value]); });
     }
   }
 
-  // Before the first put8: the residual is there.
-  __device__ __forceinline__ void ready(const ProductArgs& a) {
+  // f(piece, size, byte of the line) for pieces of 2, 4 or 8 bytes, as long as their addresses allow, of
+  // what of a row at `off` lies in no whole unit.
+  template <class F>
+  __device__ __forceinline__ void edges(int off, F f) const {
+    const int end = off + cols * 2;
+    if (off) pieces<0>(off, min(end, 16), f);
+    pieces<6>(max(end & ~15, off ? 16 : 0), end, f);
+  }
+
+  template <int kFirst, class F>
+  static __device__ __forceinline__ void pieces(int b, int end, F f) {
+    auto piece = [&](auto index, auto size) {
+      constexpr int kIndex = decltype(index)::value, kBytes = decltype(size)::value;
+      if ((kIndex >= 3 || (b & kBytes)) && b + kBytes <= end) {
+        f(std::integral_constant<int, kFirst + kIndex>{}, size, b);
+        b += kBytes;
+      }
+    };
+    piece(std::integral_constant<int, 0>{}, std::integral_constant<int, 2>{});
+    piece(std::integral_constant<int, 1>{}, std::integral_constant<int, 4>{});
+    piece(std::integral_constant<int, 2>{}, std::integral_constant<int, 8>{});
+    piece(std::integral_constant<int, 3>{}, std::integral_constant<int, 8>{});
+    piece(std::integral_constant<int, 4>{}, std::integral_constant<int, 4>{});
+    piece(std::integral_constant<int, 5>{}, std::integral_constant<int, 2>{});
+  }
+
+  // Before the first put8: the residual is there, from the start of the lines.
+  __device__ __forceinline__ void ready(const ProductArgs& a, int width) {
     if (!a.add) return;
     asm volatile("cp.async.wait_all;" ::: "memory");
     __syncwarp();
+    const int off = kWhole ? 0 : off16(add_row(a, lane));
+    if (off == 0) return;
+    uint4* line = reinterpret_cast<uint4*>(lines + lane * kPitch);
+    uint4 now = line[0];
+#pragma unroll 2
+    for (int u = 0; u < width / 8; ++u) {
+      const uint4 next = line[u + 1];
+      line[u] = bytes_at(now, next, off);
+      now = next;
+    }
   }
 
+  // Columns c .. c + 7.
   __device__ __forceinline__ void put8(const ProductArgs& a, int c, float (&x)[8]) {
     uint4* p = reinterpret_cast<uint4*>(lines + lane * kPitch + c * 2);
     if (a.add) {
@@ -213,23 +293,37 @@ struct RowsOut {
     *p = make_uint4(pack2(x[0], x[1]), pack2(x[2], x[3]), pack2(x[4], x[5]), pack2(x[6], x[7]));
   }
 
-  __device__ __forceinline__ void send(const ProductArgs& a) {
-    if (bulk) {
-      if (row0 + lane < r1 && cols > 0) {
-        asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
-        asm volatile("cp.async.bulk.global.shared::cta.bulk_group [%0], [%1], %2;" ::"l"(
-                         a.Y + static_cast<int64_t>(row0 + lane) * a.ldy + col),
-                     "r"(smem_u32(lines + lane * kPitch)), "r"(cols * 2)
-                     : "memory");
+  // After the last put8.
+  __device__ __forceinline__ void send(const ProductArgs& a, int width) {
+    uint8_t* line = lines + lane * kPitch;
+    int off = 0, lo = 0, hi = cols * 2;
+    if (!kWhole) {
+      off = off16(a.Y + static_cast<int64_t>(row0 + lane) * a.ldy + col);
+      lo = off ? 16 : 0;
+      hi = (off + cols * 2) & ~15;
+      if (off) {  // to the row's own distance from a boundary
+        uint4* units = reinterpret_cast<uint4*>(line);
+        uint4 now = make_uint4(0, 0, 0, 0);
+#pragma unroll 2
+        for (int u = width / 8; u > 0; --u) {
+          const uint4 before = units[u - 1];
+          units[u] = bytes_at(before, now, 16 - off);
+          now = before;
+        }
+        units[0] = bytes_at(now, now, 16 - off);
       }
-      asm volatile("cp.async.bulk.commit_group;" ::: "memory");
-    } else {
-      __syncwarp();
-      const int rows = min(32, r1 - row0);
-      for (int r = 0; r < rows; ++r)
-        for (int c = lane; c < cols; c += 32)
-          a.Y[static_cast<int64_t>(row0 + r) * a.ldy + col + c] = reinterpret_cast<const uint16_t*>(lines + r * kPitch)[c];
     }
+    if (row0 + lane < r1 && cols > 0) {
+      uint8_t* to = reinterpret_cast<uint8_t*>(a.Y + static_cast<int64_t>(row0 + lane) * a.ldy + col) - off;
+      asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
+      if (hi > lo)
+        asm volatile("cp.async.bulk.global.shared::cta.bulk_group [%0], [%1], %2;" ::"l"(to + lo),
+                     "r"(smem_u32(line + lo)), "r"(hi - lo)
+                     : "memory");
+      if (!kWhole)
+        edges(off, [&](auto, auto size, int b) { write_piece<decltype(size)::value>(to + b, read_piece<decltype(size)::value>(line + b)); });
+    }
+    asm volatile("cp.async.bulk.commit_group;" ::: "memory");
   }
 };
 
@@ -381,7 +475,7 @@ __host__ __device__ constexpr uint32_t umma_idesc_f8(int M, int N) {
   return (1u << 4) | ((uint32_t)(N >> 3) << 17) | ((uint32_t)(M >> 4) << 24);  // f32 D, e4m3 A and B
 }
 
-template <bool kF8, bool kPair, int kBN>
+template <bool kF8, bool kPair, int kBN, bool kWhole>
 __global__ void __launch_bounds__(kTileThreads, 1)
     tile_kernel(const __grid_constant__ CUtensorMap tmX, const __grid_constant__ CUtensorMap tmW,
                 const __grid_constant__ CUtensorMap tmWlo, const __grid_constant__ ProductArgs args) {
@@ -394,7 +488,7 @@ __global__ void __launch_bounds__(kTileThreads, 1)
   const int warp = __shfl_sync(0xffffffffu, static_cast<int>(threadIdx.x >> 5), 0);  // warp-uniform
   const int lane = threadIdx.x & 31;
   // A cluster is a pair of CTAs that share a 256-row tile, or args.split CTAs that share K.
-  const bool split = !kPair && args.split > 1;
+  const bool split = C::kCanSplit && args.split > 1;
   const uint32_t cta = kPair || split ? cluster_ctarank() : 0u;
   const uint32_t rank = kPair ? cta : 0u;
 
@@ -658,7 +752,7 @@ __global__ void __launch_bounds__(kTileThreads, 1)
       const int row0 = u.m0 + static_cast<int>(rank) * kRowTile + quarter * 32;  // the warp's 32 rows
       const int col0 = u.n0 + half * kNC;
       if constexpr (kF8) {
-        RowsOut<kNC> rows_out;
+        RowsOut<kNC, kWhole> rows_out;
         if (!split) rows_out.begin(args, out_buf, row0, u.r1, col0, kNC, lane);
         float acc[kNC];
 #pragma unroll
@@ -725,7 +819,7 @@ __global__ void __launch_bounds__(kTileThreads, 1)
             part[c * kRowTile] = make_float4(acc[4 * c], acc[4 * c + 1], acc[4 * c + 2], acc[4 * c + 3]);
           break;
         }
-        rows_out.ready(args);
+        rows_out.ready(args, kNC);
 #pragma unroll
         for (int c = 0; c < kNC; c += 8) {
           float x[8];
@@ -733,13 +827,13 @@ __global__ void __launch_bounds__(kTileThreads, 1)
           for (int j = 0; j < 8; ++j) x[j] = acc[c + j];
           rows_out.put8(args, c, x);
         }
-        rows_out.send(args);
+        rows_out.send(args, kNC);
       } else {
-        RowsOut<kNC> rows_out;
+        RowsOut<kNC, kWhole> rows_out;
         if (!split) rows_out.begin(args, out_buf, row0, u.r1, col0, kNC, lane);
         if (!wait_bar(my_tfull + 8 * C::kHalves * acc_buf, acc_phase, abort_flag, status, args.timeout_ns)) break;
         tc_fence_after();
-        if (!split) rows_out.ready(args);
+        if (!split) rows_out.ready(args, kNC);
 #pragma unroll 1
         for (int g = 0; g < kNC / 32; ++g) {
           uint32_t r[32];
@@ -764,7 +858,7 @@ __global__ void __launch_bounds__(kTileThreads, 1)
           }
         }
         if (split) break;
-        rows_out.send(args);
+        rows_out.send(args, kNC);
         if (++acc_buf == C::kAccs) {
           acc_buf = 0;
           acc_phase ^= 1;
@@ -774,27 +868,43 @@ __global__ void __launch_bounds__(kTileThreads, 1)
     if (split) {
       // Every CTA of the cluster adds its columns of the tile over the shares, in order.
       // (The operand stages are free: the accumulator's last hand-over follows every MMA.)
-      cluster_sync_all();
-      if (ok && unit0 < num_units) {
+      const bool work = ok && unit0 < num_units;
+      const int per = kBN / (2 * args.split);  // columns per thread: 32 or 16
+      const int c0 = static_cast<int>(cta) * 2 * per + half * per;
+      RowsOut<kNC, kWhole> rows_out;
+      if (work) {
         const Unit u = find_unit(args, sm->cum, unit0, num_n, C::kBM, kBN);
-        const int per = kBN / (2 * args.split);  // columns per thread: 32, 16 or 8
-        const int r = quarter * 32 + lane;
-        const int c0 = static_cast<int>(cta) * 2 * per + half * per;
-        RowsOut<kNC> rows_out;
         rows_out.begin(args, out_buf, u.m0 + quarter * 32, u.r1, u.n0 + c0, per, lane);
-        rows_out.ready(args);
-        for (int c = 0; c < per; c += 8) {
-          float x[8];
-          for (int k = 0; k < args.split; ++k) {
-            const uint32_t p = mapa_shared(smem_u32(smem) + (((c0 + c) / 4) * kRowTile + r) * 16, k);
-            const float4 a = ld_cluster(p), b = ld_cluster(p + kRowTile * 16);
-            const float v[8] = {a.x, a.y, a.z, a.w, b.x, b.y, b.z, b.w};
+      }
+      cluster_sync_all();
+      if (work) {
+        rows_out.ready(args, per);
+        const uint32_t mine = smem_u32(smem) + (c0 / 4 * kRowTile + quarter * 32 + lane) * 16;
+        auto put = [&](auto shares) {
+          constexpr int kShares = decltype(shares)::value, kPer = kBN / (2 * kShares);
+          float4 v[kPer / 4][kShares];  // all in flight at once
 #pragma unroll
-            for (int j = 0; j < 8; ++j) x[j] = k == 0 ? v[j] : __fadd_rn(x[j], v[j]);
+          for (int c = 0; c < kPer / 4; ++c)
+#pragma unroll
+            for (int k = 0; k < kShares; ++k) v[c][k] = ld_cluster(mapa_shared(mine + c * kRowTile * 16, k));
+#pragma unroll
+          for (int c = 0; c < kPer / 4; c += 2) {
+            float x[8];
+#pragma unroll
+            for (int k = 0; k < kShares; ++k) {
+              const float4 a = v[c][k], b = v[c + 1][k];
+              const float y[8] = {a.x, a.y, a.z, a.w, b.x, b.y, b.z, b.w};
+#pragma unroll
+              for (int j = 0; j < 8; ++j) x[j] = k == 0 ? y[j] : __fadd_rn(x[j], y[j]);
+            }
+            rows_out.put8(args, c * 4, x);
           }
-          rows_out.put8(args, c, x);
-        }
-        rows_out.send(args);
+        };
+        if (args.split == 2)
+          put(std::integral_constant<int, 2>{});
+        else
+          put(std::integral_constant<int, 4>{});
+        rows_out.send(args, per);
       }
       cluster_sync_all();  // no CTA leaves while another reads its shares
     }
@@ -1093,10 +1203,10 @@ int64_t units_at_most(const ProductArgs& a, int bm, int bn) {
   return ((static_cast<int64_t>(a.n) + bm - 1) / bm + a.experts - 1) * ((a.out + bn - 1) / bn);
 }
 
-template <bool kF8, bool kPair, int kBN>
-cudaError_t launch_tile(ProductArgs a, const DeviceInfo& d, cudaStream_t st, int split = 1) {
+template <bool kF8, bool kPair, int kBN, bool kWhole>
+cudaError_t launch_tile_as(ProductArgs a, const DeviceInfo& d, cudaStream_t st, int split) {
   using C = TileCfg<kF8, kPair, kBN>;
-  auto* fn = tile_kernel<kF8, kPair, kBN>;
+  auto* fn = tile_kernel<kF8, kPair, kBN, kWhole>;
   // Per kernel and device: the resident units (CTAs or pairs), once its
   // shared-memory limit is raised.  0: not yet done.
   static std::atomic<int> resident[64];
@@ -1126,7 +1236,7 @@ cudaError_t launch_tile(ProductArgs a, const DeviceInfo& d, cudaStream_t st, int
   }
   // At most this many units have work; with offsets on the device the exact number is not known here.
   const int64_t most = units_at_most(a, C::kBM, kBN);
-  while (split > a.nkb) split /= 2;
+  while (split > a.nkb) split /= 2;  // 1, 2 or 4
   a.split = split;
   if (most < units || split > 1) units = static_cast<int>(most);
   CUtensorMap mx, mw, mlo;
@@ -1141,6 +1251,12 @@ cudaError_t launch_tile(ProductArgs a, const DeviceInfo& d, cudaStream_t st, int
   const int cluster = kPair ? 2 : split;
   return launch_chained(fn, dim3(static_cast<unsigned>(cluster * units)), dim3(kTileThreads), C::kSmemBytes, cluster, st,
                         mx, mw, mlo, a);
+}
+
+template <bool kF8, bool kPair, int kBN>
+cudaError_t launch_tile(const ProductArgs& a, const DeviceInfo& d, cudaStream_t st, int split = 1) {
+  return a.vec_y && a.out % 8 == 0 ? launch_tile_as<kF8, kPair, kBN, true>(a, d, st, split)
+                                   : launch_tile_as<kF8, kPair, kBN, false>(a, d, st, split);
 }
 
 // Which kernel.  Both operand types, times on one B200 in us (e4m3 unless said).
@@ -1172,11 +1288,11 @@ cudaError_t launch_type(const ProductArgs& a, const DeviceInfo& d, cudaStream_t 
   if (per <= (one ? 8 : 4)) return launch_skinny<kF8, 1, 2, 2>(a, d, st);
   if (per <= (one ? 16 : 8)) return launch_skinny<kF8, 2, 2, 2>(a, d, st);
   // Small products of more rows, 32 a pass and the passes side by side: the work in blocks of 16 x 32 x 128
-  // bytes.  Times of the two kernels: 64 rows, 1024 -> 1000: 3.8 and 9.3; 32, 4096 -> 4096: 9.7 and 13.6;
-  // 1000, 256 -> 512: 9.8 and 8.7 (the rule's edge); 8 experts, 96 rows in all, 1024 -> 1024: 7.7 and 11.3.
+  // bytes, one of each of the CTA's 8 warps at least.  Times of the two kernels: 64 rows, 1024 -> 1000: 3.8 and 9.3; 32, 4096 -> 4096: 9.7 and 13.6;
+  // 3802, 128 -> 1026: 49 and 13.6; 8 experts, 96 rows in all, 1024 -> 1024: 7.7 and 11.3.
   const int64_t active = a.experts < a.n ? a.experts : a.n;
   const int64_t passes = one ? (per + 31) / 32 : a.n / 32 + active;
-  if (passes * strips * a.nkb <= 8192) return launch_skinny<kF8, 4, 1, 2>(a, d, st);
+  if (passes * strips * (a.nkb > 8 ? a.nkb : 8) <= 8192) return launch_skinny<kF8, 4, 1, 2>(a, d, st);
   // Row blocks: exact for one expert, else half a block more per expert, and one at least.
   auto waves = [&](int bm, int bn, int resident) {
     const int64_t cols = (a.out + bn - 1) / bn;

@@ -487,6 +487,39 @@ def test_layer_captured_and_on_another_stream(ar):
     assert torch.equal(out, want2)
 
 
+@pytest.mark.parametrize("kind", ["scaled", "bf16"])
+@pytest.mark.parametrize("n,inn,out", [(2048, 128, 2300), (1100, 256, 3901), (2000, 1152, 301), (150, 8192, 603), (600, 2176, 1502),
+                                       (150, 8192, 2)])
+def test_rows_of_the_output_at_every_offset(ar, n, inn, out, kind):
+    """Y and the residual at any distance from a 16-byte boundary, over the tiles' shapes and splits: the
+    values of an aligned call, and nothing beside the rows."""
+    wide = (out + 7) // 8 * 8
+    x, w, res = rand(1, n, inn), rand(2, wide, inn, std=0.05), rand(3, n, wide)
+    if kind == "scaled":
+        xq, wq = ar.quant_scaled(x), ar.quant_scaled(w, 128)
+        ws = wq[1][:(out + 127) // 128]
+
+        def run(o, **kw):
+            return ar.linear_scaled(*xq, wq[0][:o], wq[1] if o == wide else ws, **kw)
+    else:
+        offsets = torch.tensor([0, n], dtype=torch.int32, device="cuda")
+
+        def run(o, add=None, **kw):
+            return ar.grouped_linear(x, offsets, w[None, :o], **kw)
+    plain, added = run(wide), run(wide, add=res)
+    for y_off, add_off, gap in [(0, 1, 3), (1, 0, 0), (3, 3, 8), (7, 2, 1), (2, 7, 2), (4, 5, 4), (5, 4, 16), (6, 6, 9), (1, None, 5)]:
+        buf = torch.full((n * (out + gap) + 16,), 7.0, dtype=torch.bfloat16, device="cuda")
+        y = buf[y_off:].as_strided((n, out), (out + gap, 1))
+        add = None
+        if add_off is not None:
+            add = torch.zeros(n * (out + 3) + 16, dtype=torch.bfloat16, device="cuda")[add_off:].as_strided((n, out), (out + 3, 1))
+            add.copy_(res[:, :out])
+        run(out, add=add, out=y)
+        assert torch.equal(y, (plain if add is None else added)[:, :out]), (y_off, add_off, gap)
+        y.fill_(7.0)
+        assert bool((buf == 7.0).all()), (y_off, add_off, gap)
+
+
 def test_launches_in_a_row_are_ordered(ar):
     """Layers back to back, each over the buffers of the one before: as with a synchronisation between
     them, in a stream and in a graph (the launches overlap their starts)."""
