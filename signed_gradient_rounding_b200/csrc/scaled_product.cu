@@ -185,9 +185,9 @@ __device__ __forceinline__ void write_piece(uint8_t* p, uint2 v) {
 // Where rows or widths are not multiples of 16 bytes, a line is brought as far from a 16-byte
 // boundary as its row in memory is, so that the whole units of the row still leave by one bulk copy (and
 // come, for the residual, by 16-byte copies); the up to 7 elements before and after them are moved
-// in pieces of 2, 4 and 8 bytes.  A kernel of its own (not kWhole): within the other one's, that code
-// took registers from its loop over K (76 rows, 4096 -> 11008: 21.8 us for 19.2).  (All elements one by one, by the whole warp: 4574 rows, 608 -> 2785: 36 us, 26 so, 20 with
-// aligned rows.)
+// in pieces of 2, 4 and 8 bytes.  (All elements one by one, by the whole warp: 4574 rows, 608 ->
+// 2785: 36 us; so, 26; 20 with aligned rows.)  This form (not kWhole) has a kernel of its own:
+// within the aligned one, its code slowed the loop over K (76 rows, 4096 -> 11008: 21.8 us for 19.2).
 template <int kNC, bool kWhole>
 struct RowsOut {
   static constexpr int kPitch = kNC * 2 + 16;
