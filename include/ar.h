@@ -441,8 +441,9 @@ ar_status ar_quant_scaled(const void* x, ar_dtype x_dtype, int64_t ldx, int64_t 
                           void* stream);
 
 /* silu(a) * b in fp32 (as ar_silu_mul, without its rounding to bf16) as a scaled tensor
- * with row blocks.  a, b: [rows, cols] bf16, pitches lda, ldb (two halves of one
- * gate-and-up output, for example). */
+ * with row blocks; a silu below the smallest normal number (a < -91.9) counts as 0.
+ * a, b: [rows, cols] bf16, pitches lda, ldb (two halves of one gate-and-up output,
+ * for example). */
 ar_status ar_silu_mul_scaled(const uint16_t* a, int64_t lda, const uint16_t* b, int64_t ldb, int64_t rows,
                              int64_t cols, uint8_t* q, int64_t ldq, float* scale, void* stream);
 

@@ -428,16 +428,18 @@ bool aligned_to(const void* p, uintptr_t a) { return reinterpret_cast<uintptr_t>
 template <bool kVec>
 constexpr int kUnitsOf = kVec ? 4 : 1;
 
-// silu(f) = f / (1 + exp(-f)), from the hardware's exponential and reciprocal: relative error
-// below 2^-21 + |f| 2^-23 (the argument f log2(e) is rounded once; ex2 and rcp are within 2
-// units).  With the library's expf and division the kernel was bound by its instructions:
-// 33 per element, 217 us for 16384 x 11008 where the memory takes 139.  exp(-f) = inf gives
-// f * 0 = -0, the limit.
+// silu(f) = f / (1 + exp(-f)), from the hardware's exponential and reciprocal, as (f / 128) times
+// 1 / (1/128 + exp(-f) / 128): so the reciprocal is a normal number wherever silu is one (down to
+// f = -91.9; of the plain sum it is subnormal from -87.3 on, and the approximation gives 0 for
+// those).  f / 128 is exact for every bf16.  Relative error below 2^-20 + |f| 2^-23: the argument
+// f log2(e) - 7 is rounded once, ex2 and rcp are within 2 units.  With the library's expf and
+// division the kernel was bound by its instructions: 33 per element, 217 us for 16384 x 11008
+// where the memory takes 139.  exp(-f) = inf gives f * 0 = -0, the limit.
 __device__ __forceinline__ float silu(float f) {
   float e, r;
-  asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(e) : "f"(__fmul_rn(f, -1.44269504088896341f)));
-  asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(r) : "f"(__fadd_rn(1.0f, e)));
-  return __fmul_rn(f, r);
+  asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(e) : "f"(__fmaf_rn(f, -1.44269504088896341f, -7.0f)));
+  asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(r) : "f"(__fadd_rn(0x1p-7f, e)));
+  return __fmul_rn(__fmul_rn(f, 0x1p-7f), r);
 }
 
 template <bool kXBf16, bool kGated, bool kVec>
