@@ -61,6 +61,10 @@ struct TileQuantArgs {
 // own blocks have (chain_next), and waits for the one before it to complete, its writes
 // visible, before it touches memory (chain_wait, by every thread of every block, first of
 // all).  A launch without the attribute before or after it is ordered as ever.
+//
+// So a kernel is already running while the one before it writes what it will read.  The read-only
+// path (.nc loads, the ldg intrinsic) promises data that does not change while the kernel
+// runs, and leaves the compiler free to move the load across the wait: no kernel of the chain uses it.
 #ifdef __CUDACC__
 __device__ __forceinline__ void chain_next() { asm volatile("griddepcontrol.launch_dependents;" ::: "memory"); }
 __device__ __forceinline__ void chain_wait() { asm volatile("griddepcontrol.wait;" ::: "memory"); }

@@ -37,8 +37,8 @@ __device__ __forceinline__ void expert_rows(const ProductArgs& a, int e, int& r0
     r1 = a.n;
     return;
   }
-  r0 = min(max(__ldg(a.offsets + e), 0), a.n);
-  r1 = min(max(__ldg(a.offsets + e + 1), r0), a.n);
+  r0 = min(max(a.offsets[e], 0), a.n);
+  r1 = min(max(a.offsets[e + 1], r0), a.n);
 }
 
 // ---------------------------------------------------------------------------
@@ -1061,13 +1061,13 @@ __global__ void __launch_bounds__(32 * kSkinnyWarps) skinny_kernel(const __grid_
           }
         }
         if (kF8) {
-          sw[j] = __ldg(ws + kb);
+          sw[j] = ws[kb];
 #pragma unroll
           for (int nt = 0; nt < kNT; ++nt)
 #pragma unroll
             for (int h = 0; h < 2; ++h) {
               const int row = t0 + nt * 8 + q * 2 + h;
-              sx[j][nt][h] = row < r1 ? __ldg(a.xs + static_cast<int64_t>(row) * a.nkb + kb) : 0.f;
+              sx[j][nt][h] = row < r1 ? a.xs[static_cast<int64_t>(row) * a.nkb + kb] : 0.f;
             }
         }
       }

@@ -46,9 +46,10 @@ struct OctOf<true, false> {
   using type = Bf16Raw;
 };
 
-__device__ __forceinline__ uint4 ldg_stream(const void* p) {
+// Read once.  (Not .nc: see chain_wait.)
+__device__ __forceinline__ uint4 ld_stream(const void* p) {
   uint4 v;
-  asm volatile("ld.global.nc.L1::no_allocate.v4.u32 {%0, %1, %2, %3}, [%4];"
+  asm volatile("ld.global.L1::no_allocate.v4.u32 {%0, %1, %2, %3}, [%4];"
                : "=r"(v.x), "=r"(v.y), "=r"(v.z), "=r"(v.w)
                : "l"(p));
   return v;
@@ -67,15 +68,15 @@ struct Place {
 __device__ __forceinline__ int place_col(const Place& p, int k) { return (k < 4 ? p.col0 : p.col1) + 32 * (k & 3); }
 __device__ __forceinline__ int64_t place_at(const Place& p, int k) { return (k < 4 ? p.row0 : p.row1) + place_col(p, k); }
 
-// Elements at or past `cols` read as 0.  The plain ld (not .nc) is for inputs that may be
-// the buffer the same kernel writes (kAlias).
+// Elements at or past `cols` read as 0.  kAlias: loads that the compiler orders with the stores
+// around them, for inputs that may be the buffer the same kernel writes.
 template <bool kVec, bool kAlias = false>
 __device__ __forceinline__ typename OctOf<true, kVec>::type load_oct(const uint16_t* p, const Place& at, int cols) {
   typename OctOf<true, kVec>::type o;
   if constexpr (kVec) {
     o.v = make_uint4(0, 0, 0, 0);
     if (at.col0 < cols)
-      o.v = kAlias ? *reinterpret_cast<const uint4*>(p + at.row0 + at.col0) : ldg_stream(p + at.row0 + at.col0);
+      o.v = kAlias ? *reinterpret_cast<const uint4*>(p + at.row0 + at.col0) : ld_stream(p + at.row0 + at.col0);
   } else {
 #pragma unroll
     for (int k = 0; k < 8; ++k) o.e[k] = place_col(at, k) < cols ? p[place_at(at, k)] : uint16_t(0);
@@ -95,7 +96,7 @@ __device__ __forceinline__ F32Oct load_oct(const float* p, const Place& at, int 
       o.a = *reinterpret_cast<const float4*>(q);
       o.b = *reinterpret_cast<const float4*>(q + 4);
     } else {
-      const uint4 x = ldg_stream(q), y = ldg_stream(q + 4);
+      const uint4 x = ld_stream(q), y = ld_stream(q + 4);
       o.a = make_float4(__uint_as_float(x.x), __uint_as_float(x.y), __uint_as_float(x.z), __uint_as_float(x.w));
       o.b = make_float4(__uint_as_float(y.x), __uint_as_float(y.y), __uint_as_float(y.z), __uint_as_float(y.w));
     }
