@@ -247,7 +247,7 @@ PyObject* rms_norm(PyObject*, PyObject* const* a, Py_ssize_t nargs) {
         h = tensor(a[6], "sum_out");
         lds = pitch(h, "sum_out", dev, rows, cols);
         typed(h, "sum_out", r.scalar_type());
-        if (h.data_ptr() == x.data_ptr()) throw Refused("sum_out must not be x");
+        if (x.numel() > 0 && h.data_ptr() == x.data_ptr()) throw Refused("sum_out must not be x");
       }
     } else if (!none(a[6])) {
       throw Refused("sum_out needs a residual");

@@ -59,3 +59,32 @@ def test_silu_left_end_in_a_block_of_its_own(ar):
     assert ((s.double() - top).abs() <= top * 150 * U + 2.0 ** -149).all()
     u = v / s.double()
     assert ((q.double() - u).abs() <= u.abs() * (2.0 ** -4 + 300 * U)).all()
+
+
+@pytest.mark.parametrize("rows,cols", [(0, 512), (3, 0), (0, 0)])
+def test_empty_batches(ar, rows, cols):
+    """No rows or no columns: every call returns at once, the norm with the residual in place among them."""
+    x, r = (torch.ones(rows, cols, dtype=torch.bfloat16, device="cuda") for _ in range(2))
+    for sum_out in (None, r, torch.empty_like(r)):
+        y, q, s, h = ar.rms_norm(x, None, 1e-6, residual=r, want_scaled=True, sum_out=sum_out)
+        assert y.shape == q.shape == h.shape == (rows, cols) and s.shape == (rows, (cols + 127) // 128)
+        assert sum_out is None or h is sum_out
+    for block_rows in (1, 128):
+        q, s = ar.quant_scaled(x, block_rows)
+        assert q.shape == (rows, cols) and s.shape == (-(-rows // block_rows), (cols + 127) // 128)
+    assert ar.silu_mul_scaled(x, r)[0].shape == (rows, cols)
+
+
+def test_products_of_no_rows(ar):
+    w = torch.ones(2, 24, 512, dtype=torch.bfloat16, device="cuda")
+    wq, ws = ar.quant_scaled(w, 128)
+    x = torch.empty(0, 512, dtype=torch.bfloat16, device="cuda")
+    q, s = ar.quant_scaled(x)
+    offsets = torch.zeros(3, dtype=torch.int32, device="cuda")
+    add, out = (torch.empty(0, 24, dtype=torch.bfloat16, device="cuda") for _ in range(2))
+    for o in (None, out):
+        assert ar.linear_scaled(q, s, wq[0], ws[0], out=o).shape == (0, 24)
+        assert ar.linear_scaled(q, s, wq[0], ws[0], add=add, out=o).shape == (0, 24)
+        assert ar.grouped_linear(x, offsets, w, out=o).shape == (0, 24)
+        assert ar.grouped_linear_scaled(q, s, offsets, wq, ws, out=o).shape == (0, 24)
+    assert ar.linear_scaled(q, s, wq[0], ws[0], add=add, out=add) is add
