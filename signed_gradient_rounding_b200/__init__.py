@@ -274,7 +274,8 @@ def silu_mul(a: torch.Tensor, b: torch.Tensor, stream=None) -> torch.Tensor:
 # The 8-bit chain.  A scaled tensor is (q float8_e4m3fn [rows, cols], scale fp32
 # [rows, ceil(cols/128)] for activations or [ceil(rows/128), ceil(cols/128)] for
 # weights).  Tensors may have a row pitch (a slice of wider rows); their columns are
-# contiguous.  Calls run on the tensors' device, on its current stream by default.
+# contiguous.  Calls run on the tensors' device, on its current stream by default.  On a given
+# stream, new tensors come from that stream's pool: it need wait for nothing but the call's inputs.
 # Checks, output allocation and the call itself are in the compiled _binding module;
 # a refused argument raises ValueError, a status of the library ArError.
 # ---------------------------------------------------------------------------

@@ -13,6 +13,7 @@
 #include <c10/cuda/CUDAStream.h>
 
 #include <initializer_list>
+#include <optional>
 #include <stdexcept>
 #include <string>
 
@@ -111,26 +112,45 @@ at::Tensor empty(at::IntArrayRef shape, at::ScalarType dtype, int dev) {
   return at::detail::empty_cuda(shape, dtype, c10::Device(c10::kCUDA, dev), std::nullopt);
 }
 
-// The call's stream: a torch.cuda.Stream, or the device's current one (None).
-void* stream_of(PyObject* o, int dev) {
-  if (none(o)) return c10::cuda::getCurrentCUDAStream(dev).stream();
-  PyObject* v = PyObject_GetAttrString(o, "cuda_stream");
-  if (!v) throw Raised();
-  void* p = PyLong_AsVoidPtr(v);
-  Py_DECREF(v);
-  if (PyErr_Occurred()) throw Raised();
-  return p;
-}
+// The call's stream: a torch.cuda.Stream, or the device's current one (None).  A given stream is the
+// current one while this lives, so that the call's new tensors come from its pool: memory that was
+// freed on another stream may still be in use there.
+class CallStream {
+ public:
+  CallStream(PyObject* o, int dev) : before_(c10::cuda::getCurrentCUDAStream(static_cast<c10::DeviceIndex>(dev))) {
+    if (none(o)) {
+      ptr_ = before_.stream();
+      return;
+    }
+    PyObject* v = PyObject_GetAttrString(o, "cuda_stream");
+    if (!v) throw Raised();
+    ptr_ = PyLong_AsVoidPtr(v);
+    Py_DECREF(v);
+    if (PyErr_Occurred()) throw Raised();
+    guard_.emplace(c10::cuda::getStreamFromExternal(static_cast<cudaStream_t>(ptr_), static_cast<c10::DeviceIndex>(dev)));
+  }
+  void* get() const { return ptr_; }
 
-// The call's tensors were used on a stream of the caller's choice: their memory is not handed
-// out again before that stream is done with them.
-void used_on(PyObject* stream, void* ptr, int dev, std::initializer_list<const at::Tensor*> tensors) {
-  if (none(stream)) return;
-  const auto s = c10::cuda::getStreamFromExternal(static_cast<cudaStream_t>(ptr), static_cast<c10::DeviceIndex>(dev));
-  for (const at::Tensor* t : tensors)
-    if (t && t->defined() && t->numel() > 0)
-      c10::cuda::CUDACachingAllocator::recordStream(t->storage().data_ptr(), s);
-}
+  // After the launch on a given stream: the memory of the tensors that it was given is not handed out
+  // again before that stream is done with them, nor that of the new ones, which the caller goes on to
+  // use on the stream that was current, before that one is.
+  void used(std::initializer_list<const at::Tensor*> given, std::initializer_list<const at::Tensor*> made) const {
+    if (!guard_) return;
+    record(given, guard_->current_stream());
+    record(made, before_);
+  }
+
+ private:
+  static void record(std::initializer_list<const at::Tensor*> tensors, c10::cuda::CUDAStream stream) {
+    for (const at::Tensor* t : tensors)
+      if (t && t->defined() && t->numel() > 0)
+        c10::cuda::CUDACachingAllocator::recordStream(t->storage().data_ptr(), stream);
+  }
+
+  c10::cuda::CUDAStream before_;
+  std::optional<c10::cuda::CUDAStreamGuard> guard_;
+  void* ptr_ = nullptr;
+};
 
 const at::Tensor* maybe(PyObject* o) { return none(o) ? nullptr : &THPVariable_Unpack(o); }
 
@@ -227,6 +247,7 @@ PyObject* rms_norm(PyObject*, PyObject* const* a, Py_ssize_t nargs) {
   return guarded(nargs, 8, [&]() -> PyObject* {
     const at::Tensor& x = tensor(a[0], "x");
     const int dev = device_of(x, "x");
+    const CallStream st(a[7], dev);
     const ar_dtype xd = dtype_of(x, "x");
     const int64_t ldx = pitch(x, "x"), rows = x.size(0), cols = x.size(1);
     const double eps = PyFloat_AsDouble(a[2]);
@@ -264,15 +285,14 @@ PyObject* rms_norm(PyObject*, PyObject* const* a, Py_ssize_t nargs) {
       q = empty({rows, cols}, kE4m3, dev);
       s = empty({rows, blocks_of(cols)}, at::kFloat, dev);
     }
-    void* st = stream_of(a[7], dev);
     launch(dev, "ar_rms_norm", [&] {
       return ar_rms_norm(x.data_ptr(), xd, ldx, rows, cols, rp, rd, ldr, wp, wd, static_cast<float>(eps),
                          h.defined() ? h.data_ptr() : nullptr, lds,
                          want_y ? static_cast<uint16_t*>(y.data_ptr()) : nullptr, cols,
                          want_q ? static_cast<uint8_t*>(q.data_ptr()) : nullptr, cols,
-                         want_q ? s.data_ptr<float>() : nullptr, st);
+                         want_q ? s.data_ptr<float>() : nullptr, st.get());
     });
-    used_on(a[7], st, dev, {&x, maybe(a[1]), maybe(a[3]), &y, &q, &s, &h});
+    st.used({&x, maybe(a[1]), maybe(a[3]), maybe(a[6])}, {&y, &q, &s, none(a[6]) ? &h : nullptr});
     return wrap_all(y, q, s, h);
   });
 }
@@ -283,6 +303,7 @@ PyObject* quant_scaled(PyObject*, PyObject* const* a, Py_ssize_t nargs) {
     const at::Tensor& x = tensor(a[0], "x");
     const int dev = device_of(x, "x");
     const ar_dtype xd = dtype_of(x, "x");
+    const CallStream st(a[2], dev);
     const int64_t block_rows = integer(a[1]);
     const bool stack = x.dim() == 3;
     const int64_t ldx = stack ? stack_pitch(x, "x") : pitch(x, "x");
@@ -290,12 +311,11 @@ PyObject* quant_scaled(PyObject*, PyObject* const* a, Py_ssize_t nargs) {
     const int64_t rb = block_rows == 1 ? rows : blocks_of(rows), cb = blocks_of(cols);
     at::Tensor q = empty(x.sizes(), kE4m3, dev);
     at::Tensor s = stack ? empty({count, rb, cb}, at::kFloat, dev) : empty({rb, cb}, at::kFloat, dev);
-    void* st = stream_of(a[2], dev);
     launch(dev, "ar_quant_scaled", [&] {
       return ar_quant_scaled(x.data_ptr(), xd, ldx, count, rows, cols, static_cast<int32_t>(block_rows),
-                             static_cast<uint8_t*>(q.data_ptr()), cols, s.data_ptr<float>(), st);
+                             static_cast<uint8_t*>(q.data_ptr()), cols, s.data_ptr<float>(), st.get());
     });
-    used_on(a[2], st, dev, {&x, &q, &s});
+    st.used({&x}, {&q, &s});
     return wrap_all(q, s);
   });
 }
@@ -305,18 +325,18 @@ PyObject* silu_mul_scaled(PyObject*, PyObject* const* args, Py_ssize_t nargs) {
   return guarded(nargs, 3, [&]() -> PyObject* {
     const at::Tensor &a = tensor(args[0], "a"), &b = tensor(args[1], "b");
     const int dev = device_of(a, "a");
+    const CallStream st(args[2], dev);
     typed(a, "a", at::kBFloat16);
     const int64_t lda = pitch(a, "a"), rows = a.size(0), cols = a.size(1);
     const int64_t ldb = pitch(b, "b", dev, rows, cols);
     typed(b, "b", at::kBFloat16);
     at::Tensor q = empty({rows, cols}, kE4m3, dev), s = empty({rows, blocks_of(cols)}, at::kFloat, dev);
-    void* st = stream_of(args[2], dev);
     launch(dev, "ar_silu_mul_scaled", [&] {
       return ar_silu_mul_scaled(static_cast<const uint16_t*>(a.data_ptr()), lda,
                                 static_cast<const uint16_t*>(b.data_ptr()), ldb, rows, cols,
-                                static_cast<uint8_t*>(q.data_ptr()), cols, s.data_ptr<float>(), st);
+                                static_cast<uint8_t*>(q.data_ptr()), cols, s.data_ptr<float>(), st.get());
     });
-    used_on(args[2], st, dev, {&a, &b, &q, &s});
+    st.used({&a, &b}, {&q, &s});
     return wrap_all(q, s);
   });
 }
@@ -345,6 +365,7 @@ PyObject* linear_scaled(PyObject*, PyObject* const* a, Py_ssize_t nargs) {
   return guarded(nargs, 8, [&]() -> PyObject* {
     const at::Tensor &X = tensor(a[0], "Xq"), &W = tensor(a[2], "Wq");
     const int dev = device_of(X, "Xq");
+    const CallStream st(a[7], dev);
     typed(X, "Xq", kE4m3);
     typed(W, "Wq", kE4m3);
     on(W, "Wq", dev);
@@ -363,14 +384,13 @@ PyObject* linear_scaled(PyObject*, PyObject* const* a, Py_ssize_t nargs) {
     }
     int32_t* status = status_of(a[6], dev);
     at::Tensor Y = output(a[5], dev, n, out, &ldy);
-    void* st = stream_of(a[7], dev);
     launch(dev, "ar_linear_scaled", [&] {
       return ar_linear_scaled(static_cast<const uint8_t*>(X.data_ptr()), ldx, static_cast<const float*>(xs), n, in,
                               static_cast<const uint8_t*>(W.data_ptr()), ldw, static_cast<const float*>(ws), out,
                               static_cast<const uint16_t*>(add), ldadd, static_cast<uint16_t*>(Y.data_ptr()), ldy, status,
-                              st);
+                              st.get());
     });
-    used_on(a[7], st, dev, {&X, maybe(a[1]), &W, maybe(a[3]), maybe(a[4]), &Y});
+    st.used({&X, maybe(a[1]), &W, maybe(a[3]), maybe(a[4]), maybe(a[5])}, {none(a[5]) ? &Y : nullptr});
     return result(a[5], Y);
   });
 }
@@ -380,6 +400,7 @@ PyObject* grouped_linear(PyObject*, PyObject* const* a, Py_ssize_t nargs) {
   return guarded(nargs, 7, [&]() -> PyObject* {
     const at::Tensor &X = tensor(a[0], "X"), &W = tensor(a[2], "W_hi");
     const int dev = device_of(X, "X");
+    const CallStream st(a[6], dev);
     typed(X, "X", at::kBFloat16);
     typed(W, "W_hi", at::kBFloat16);
     on(W, "W_hi", dev);
@@ -400,14 +421,13 @@ PyObject* grouped_linear(PyObject*, PyObject* const* a, Py_ssize_t nargs) {
     int64_t ldy = out;
     at::Tensor Y = output(a[4], dev, n, out, &ldy);
     if (n > 0 && Y.data_ptr() == X.data_ptr()) throw Refused("out must not be X");
-    void* st = stream_of(a[6], dev);
     launch(dev, "ar_grouped_linear", [&] {
       return ar_grouped_linear(static_cast<const uint16_t*>(X.data_ptr()), ldx, n, in,
                                static_cast<const int32_t*>(offsets), experts,
                                static_cast<const uint16_t*>(W.data_ptr()), static_cast<const uint16_t*>(lo), ldw, out,
-                               static_cast<uint16_t*>(Y.data_ptr()), ldy, status, st);
+                               static_cast<uint16_t*>(Y.data_ptr()), ldy, status, st.get());
     });
-    used_on(a[6], st, dev, {&X, maybe(a[1]), &W, maybe(a[3]), &Y});
+    st.used({&X, maybe(a[1]), &W, maybe(a[3]), maybe(a[4])}, {none(a[4]) ? &Y : nullptr});
     return result(a[4], Y);
   });
 }
@@ -417,6 +437,7 @@ PyObject* grouped_linear_scaled(PyObject*, PyObject* const* a, Py_ssize_t nargs)
   return guarded(nargs, 8, [&]() -> PyObject* {
     const at::Tensor &X = tensor(a[0], "Xq"), &W = tensor(a[3], "Wq");
     const int dev = device_of(X, "Xq");
+    const CallStream st(a[7], dev);
     typed(X, "Xq", kE4m3);
     typed(W, "Wq", kE4m3);
     on(W, "Wq", dev);
@@ -429,14 +450,13 @@ PyObject* grouped_linear_scaled(PyObject*, PyObject* const* a, Py_ssize_t nargs)
     int32_t* status = status_of(a[6], dev);
     int64_t ldy = out;
     at::Tensor Y = output(a[5], dev, n, out, &ldy);
-    void* st = stream_of(a[7], dev);
     launch(dev, "ar_grouped_linear_scaled", [&] {
       return ar_grouped_linear_scaled(static_cast<const uint8_t*>(X.data_ptr()), ldx, static_cast<const float*>(xs), n, in,
                                       static_cast<const int32_t*>(offsets), experts,
                                       static_cast<const uint8_t*>(W.data_ptr()), ldw, static_cast<const float*>(ws), out,
-                                      static_cast<uint16_t*>(Y.data_ptr()), ldy, status, st);
+                                      static_cast<uint16_t*>(Y.data_ptr()), ldy, status, st.get());
     });
-    used_on(a[7], st, dev, {&X, maybe(a[1]), maybe(a[2]), &W, maybe(a[4]), &Y});
+    st.used({&X, maybe(a[1]), maybe(a[2]), &W, maybe(a[4]), maybe(a[5])}, {none(a[5]) ? &Y : nullptr});
     return result(a[5], Y);
   });
 }

@@ -88,3 +88,67 @@ def test_products_of_no_rows(ar):
         assert ar.grouped_linear(x, offsets, w, out=o).shape == (0, 24)
         assert ar.grouped_linear_scaled(q, s, offsets, wq, ws, out=o).shape == (0, 24)
     assert ar.linear_scaled(q, s, wq[0], ws[0], add=add, out=add) is add
+
+
+def calls_on(ar, seed=1, rows=300, cols=512, out=264):
+    """Every entry point as a function of a stream, its operands in hand; each returns its new tensors."""
+    gen = torch.Generator(device="cuda").manual_seed(seed)
+    x, r = (torch.randn(rows, cols, generator=gen, device="cuda").to(torch.bfloat16) for _ in range(2))
+    w = torch.randn(2, out, cols, generator=gen, device="cuda").to(torch.bfloat16)
+    xq, xs = ar.quant_scaled(x)
+    wq, ws = ar.quant_scaled(w, 128)
+    offsets = torch.tensor([0, 100, rows], dtype=torch.int32, device="cuda")
+    return dict(rms_norm=lambda s: ar.rms_norm(x, None, residual=r, want_scaled=True, stream=s),
+                quant_scaled=lambda s: ar.quant_scaled(x, stream=s),
+                silu_mul_scaled=lambda s: ar.silu_mul_scaled(x, r, stream=s),
+                linear_scaled=lambda s: (ar.linear_scaled(xq, xs, wq[0], ws[0], stream=s),),
+                grouped_linear=lambda s: (ar.grouped_linear(x, offsets, w, stream=s),),
+                grouped_linear_scaled=lambda s: (ar.grouped_linear_scaled(xq, xs, offsets, wq, ws, stream=s),))
+
+
+NAMES = ["rms_norm", "quant_scaled", "silu_mul_scaled", "linear_scaled", "grouped_linear", "grouped_linear_scaled"]
+
+
+@pytest.mark.parametrize("name", NAMES)
+def test_outputs_on_a_given_stream_take_no_memory_still_in_use(ar, name):
+    """A call on a stream that need not wait for the current one, while the current one still reads a
+    tensor that was just dropped: the call's outputs must not get that memory."""
+    call = calls_on(ar)[name]
+    want = call(None)
+    side = torch.cuda.Stream()
+    torch.cuda.synchronize()
+    for like in want:
+        held = [torch.full_like(like, 3.0, dtype=torch.float32 if like.dtype == torch.float32 else torch.uint8).view(-1)
+                if like.dtype.itemsize == 1 or like.dtype == torch.float32 else torch.full_like(like, 3.0).view(-1)
+                for _ in range(4)]
+        places = {t.data_ptr() for t in held}
+        torch.cuda._sleep(20_000_000)         # (about 10 ms)
+        copies = [t + 0 for t in held]        # queued behind it
+        del held
+        got = call(side)
+        assert not places & {t.data_ptr() for t in got}
+        torch.cuda.synchronize()
+        assert all((c == 3).all() for c in copies)
+        for g, w in zip(got, want):
+            assert torch.equal(g.view(torch.uint8), w.view(torch.uint8))
+
+
+@pytest.mark.parametrize("name", NAMES)
+def test_outputs_on_a_given_stream_may_be_dropped_by_the_current_one(ar, name):
+    """The current stream reads a call's outputs (after waiting for the call's stream) and drops them: the
+    next call on that stream does not write over them before they are read."""
+    call = calls_on(ar)[name]
+    want = call(None)
+    side = torch.cuda.Stream()
+    torch.cuda.synchronize()
+    for _ in range(3):
+        got = call(side)
+        places = {t.data_ptr() for t in got}
+        torch.cuda.current_stream().wait_stream(side)
+        torch.cuda._sleep(20_000_000)
+        copies = [g.view(torch.uint8) + 0 for g in got]
+        del got
+        assert not places & {t.data_ptr() for t in call(side)}
+        torch.cuda.synchronize()
+        for c, w in zip(copies, want):
+            assert torch.equal(c, w.view(torch.uint8))
