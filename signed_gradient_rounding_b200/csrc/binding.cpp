@@ -390,7 +390,7 @@ PyObject* linear_scaled(PyObject*, PyObject* const* a, Py_ssize_t nargs) {
                               static_cast<const uint16_t*>(add), ldadd, static_cast<uint16_t*>(Y.data_ptr()), ldy, status,
                               st.get());
     });
-    st.used({&X, maybe(a[1]), &W, maybe(a[3]), maybe(a[4]), maybe(a[5])}, {none(a[5]) ? &Y : nullptr});
+    st.used({&X, maybe(a[1]), &W, maybe(a[3]), maybe(a[4]), maybe(a[5]), maybe(a[6])}, {none(a[5]) ? &Y : nullptr});
     return result(a[5], Y);
   });
 }
@@ -427,7 +427,7 @@ PyObject* grouped_linear(PyObject*, PyObject* const* a, Py_ssize_t nargs) {
                                static_cast<const uint16_t*>(W.data_ptr()), static_cast<const uint16_t*>(lo), ldw, out,
                                static_cast<uint16_t*>(Y.data_ptr()), ldy, status, st.get());
     });
-    st.used({&X, maybe(a[1]), &W, maybe(a[3]), maybe(a[4])}, {none(a[4]) ? &Y : nullptr});
+    st.used({&X, maybe(a[1]), &W, maybe(a[3]), maybe(a[4]), maybe(a[5])}, {none(a[4]) ? &Y : nullptr});
     return result(a[4], Y);
   });
 }
@@ -456,7 +456,7 @@ PyObject* grouped_linear_scaled(PyObject*, PyObject* const* a, Py_ssize_t nargs)
                                       static_cast<const uint8_t*>(W.data_ptr()), ldw, static_cast<const float*>(ws), out,
                                       static_cast<uint16_t*>(Y.data_ptr()), ldy, status, st.get());
     });
-    st.used({&X, maybe(a[1]), maybe(a[2]), &W, maybe(a[4]), maybe(a[5])}, {none(a[5]) ? &Y : nullptr});
+    st.used({&X, maybe(a[1]), maybe(a[2]), &W, maybe(a[4]), maybe(a[5]), maybe(a[6])}, {none(a[5]) ? &Y : nullptr});
     return result(a[5], Y);
   });
 }

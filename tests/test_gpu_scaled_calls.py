@@ -152,3 +152,28 @@ def test_outputs_on_a_given_stream_may_be_dropped_by_the_current_one(ar, name):
         torch.cuda.synchronize()
         for c, w in zip(copies, want):
             assert torch.equal(c, w.view(torch.uint8))
+
+
+@pytest.mark.parametrize("name", ["linear_scaled", "grouped_linear", "grouped_linear_scaled"])
+def test_status_word_is_kept_for_a_given_stream(ar, name):
+    """A status word that is dropped while its call waits on a given stream is not handed out again."""
+    x = torch.randn(300, 512, device="cuda").to(torch.bfloat16)
+    w = torch.randn(2, 264, 512, device="cuda").to(torch.bfloat16)
+    (xq, xs), (wq, ws) = ar.quant_scaled(x), ar.quant_scaled(w, 128)
+    offsets = torch.tensor([0, 100, 300], dtype=torch.int32, device="cuda")
+    side = torch.cuda.Stream()
+    torch.cuda.synchronize()
+    status = torch.zeros(1, dtype=torch.int32, device="cuda")
+    place = status.data_ptr()
+    torch.cuda.synchronize()
+    with torch.cuda.stream(side):
+        torch.cuda._sleep(20_000_000)
+    if name == "linear_scaled":
+        ar.linear_scaled(xq, xs, wq[0], ws[0], status=status, stream=side)
+    elif name == "grouped_linear":
+        ar.grouped_linear(x, offsets, w, status=status, stream=side)
+    else:
+        ar.grouped_linear_scaled(xq, xs, offsets, wq, ws, status=status, stream=side)
+    del status
+    assert place not in [torch.empty(1, dtype=torch.int32, device="cuda").data_ptr() for _ in range(4)]
+    torch.cuda.synchronize()
