@@ -163,17 +163,18 @@ def test_status_word_is_kept_for_a_given_stream(ar, name):
     offsets = torch.tensor([0, 100, 300], dtype=torch.int32, device="cuda")
     side = torch.cuda.Stream()
     torch.cuda.synchronize()
+    call = {"linear_scaled": lambda t: ar.linear_scaled(xq, xs, wq[0], ws[0], status=t, stream=side),
+            "grouped_linear": lambda t: ar.grouped_linear(x, offsets, w, status=t, stream=side),
+            "grouped_linear_scaled": lambda t: ar.grouped_linear_scaled(xq, xs, offsets, wq, ws, status=t, stream=side)}[name]
+    call(None)  # (the first call of a kernel loads it, which takes longer than the wait below)
     status = torch.zeros(1, dtype=torch.int32, device="cuda")
     place = status.data_ptr()
     torch.cuda.synchronize()
     with torch.cuda.stream(side):
-        torch.cuda._sleep(20_000_000)
-    if name == "linear_scaled":
-        ar.linear_scaled(xq, xs, wq[0], ws[0], status=status, stream=side)
-    elif name == "grouped_linear":
-        ar.grouped_linear(x, offsets, w, status=status, stream=side)
-    else:
-        ar.grouped_linear_scaled(xq, xs, offsets, wq, ws, status=status, stream=side)
+        torch.cuda._sleep(100_000_000)  # (about 50 ms)
+    call(status)
     del status
-    assert place not in [torch.empty(1, dtype=torch.int32, device="cuda").data_ptr() for _ in range(4)]
+    places = [torch.empty(1, dtype=torch.int32, device="cuda").data_ptr() for _ in range(4)]
+    assert not side.query(), "the call's stream was done before the word was asked for"
+    assert place not in places
     torch.cuda.synchronize()
