@@ -452,8 +452,8 @@ ar_status ar_silu_mul_scaled(const uint16_t* a, int64_t lda, const uint16_t* b, 
  * each block's products summed by the tensor cores in fp32, the blocks added in fp32 in
  * order within a share of K and the shares in order, one rounding to bf16.
  *   X [n, in], W [out, in]: e4m3, 16-byte aligned, `in` and the pitches multiples of 16.
- *   add [n, out] bf16 or NULL, added in fp32;  Y [n, out] bf16 out (must not overlap add
- *   unless it is add itself with the same pitch).
+ *   add [n, out] bf16 or NULL, added in fp32;  Y [n, out] bf16 out (must not overlap an
+ *   input, unless it is add itself with the same pitch).
  *   status: as for ar_linear.
  * AR_EINVAL: NULL or misaligned pointers, bad sizes or pitches.  AR_EUNSUPPORTED: n or
  * out above 2^30.  n == 0: no-op. */
@@ -471,7 +471,7 @@ ar_status ar_linear_scaled(const uint8_t* X, int64_t ldx, const float* x_scale, 
  *   empty.  Rows of Y before offsets[0] and from offsets[experts] on are left as they were.
  *   Offsets that break this are clamped into [0, n]: no access leaves X or Y, but which
  *   rows are written is then undefined.
- *   Y [n, out] bf16 out.  status: as for ar_linear.
+ *   Y [n, out] bf16 out (must not overlap an input).  status: as for ar_linear.
  * AR_EINVAL as ar_linear_scaled; AR_EUNSUPPORTED: more than 1024 experts, n or
  * experts * out above 2^30.  n == 0: no-op. */
 ar_status ar_grouped_linear(const uint16_t* X, int64_t ldx, int64_t n, int64_t in, const int32_t* offsets,

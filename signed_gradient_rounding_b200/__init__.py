@@ -288,7 +288,7 @@ def rms_norm(x: torch.Tensor, weight: torch.Tensor | None, eps: float = 1e-6, re
              want_bf16: bool = True, want_scaled: bool = False, sum_out: torch.Tensor | None = None, stream=None):
     """h = x + residual, v = h / sqrt(mean(h^2) + eps) * weight: (v bf16 or None, q, scale of v as a
     scaled tensor or None, h in the residual's dtype or None without one).  ``sum_out`` may be the
-    residual itself (updated in place)."""
+    residual itself (updated in place); it is refused where it overlaps an input otherwise."""
     return _binding.rms_norm(x, weight, eps, residual, want_bf16, want_scaled, sum_out, stream)
 
 
@@ -306,7 +306,8 @@ def silu_mul_scaled(a: torch.Tensor, b: torch.Tensor, stream=None):
 def linear_scaled(Xq: torch.Tensor, x_scale: torch.Tensor, Wq: torch.Tensor, w_scale: torch.Tensor,
                   add: torch.Tensor | None = None, out: torch.Tensor | None = None, status: torch.Tensor | None = None,
                   stream=None) -> torch.Tensor:
-    """bf16(X W^T + add) of scaled tensors X [n, in] (row blocks) and W [out, in] (128 x 128 blocks)."""
+    """bf16(X W^T + add) of scaled tensors X [n, in] (row blocks) and W [out, in] (128 x 128 blocks).
+    ``out`` may be ``add`` itself; it is refused where it overlaps an input otherwise."""
     return _binding.linear_scaled(Xq, x_scale, Wq, w_scale, add, out, status, stream)
 
 
@@ -314,7 +315,8 @@ def grouped_linear(X: torch.Tensor, offsets: torch.Tensor, W_hi: torch.Tensor, W
                    out: torch.Tensor | None = None, status: torch.Tensor | None = None, stream=None) -> torch.Tensor:
     """Y[r] = bf16(X[r] (W_hi[e] + W_lo[e])^T) for the rows offsets[e] <= r < offsets[e+1] of expert e:
     X [n, in] bf16, W [experts, out, in] bf16, offsets int32 [experts + 1] on the device.  Rows outside
-    the experts' are left as they are in ``out`` (and undefined in a new tensor)."""
+    the experts' are left as they are in ``out`` (and undefined in a new tensor).  ``out`` is refused
+    where it overlaps an input."""
     return _binding.grouped_linear(X, offsets, W_hi, W_lo, out, status, stream)
 
 

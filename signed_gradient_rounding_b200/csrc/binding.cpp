@@ -12,6 +12,7 @@
 #include <c10/cuda/CUDAGuard.h>
 #include <c10/cuda/CUDAStream.h>
 
+#include <algorithm>
 #include <initializer_list>
 #include <optional>
 #include <stdexcept>
@@ -97,6 +98,58 @@ int64_t stack_pitch(const at::Tensor& t, const char* name) {
   if ((t.size(2) > 1 && t.stride(2) != 1) || (t.size(0) > 1 && t.stride(0) != p * t.size(1)))
     throw Refused(std::string(name) + " must have contiguous columns, and matrices that follow one another");
   return p;
+}
+
+// The bytes of a matrix.
+struct Bytes {
+  uintptr_t at;
+  int64_t rows, width, pitch;
+  bool same(const Bytes& o) const { return at == o.at && (pitch == o.pitch || rows <= 1); }
+};
+
+Bytes bytes_of(const at::Tensor& t, int64_t ld) {  // (the last axis is a row, all others are rows)
+  const int64_t el = static_cast<int64_t>(t.element_size()), cols = t.size(-1);
+  return {reinterpret_cast<uintptr_t>(t.data_ptr()), cols > 0 ? t.numel() / cols : 0, cols * el, ld * el};
+}
+
+Bytes bytes_of(const at::Tensor& t) {  // contiguous
+  return {reinterpret_cast<uintptr_t>(t.data_ptr()), 1, t.numel() * static_cast<int64_t>(t.element_size()), 0};
+}
+
+int64_t floor_div(int64_t a, int64_t b) { return a / b - (a % b < 0); }
+
+// Whether the two have a byte in common.  Rows of either may lie between rows of the other.
+bool meet(const Bytes& a, const Bytes& b) {
+  if (a.rows <= 0 || b.rows <= 0 || a.width <= 0 || b.width <= 0) return false;
+  if ((a.rows > 1 && a.pitch < a.width) || (b.rows > 1 && b.pitch < b.width)) return false;  // (the library refuses these)
+  const int64_t gap = static_cast<int64_t>(a.at - b.at);  // of a's first row behind b's
+  if (gap >= (b.rows - 1) * b.pitch + b.width || -gap >= (a.rows - 1) * a.pitch + a.width) return false;
+  if (a.rows > 1 && b.rows > 1 && a.pitch == b.pitch) {
+    // row i of a and row j of b meet where -a.width < gap + (i - j) pitch < b.width
+    const int64_t lo = floor_div(-a.width - gap, a.pitch) + 1, hi = -floor_div(gap - b.width, a.pitch) - 1;
+    return std::max(lo, 1 - b.rows) <= std::min(hi, a.rows - 1);
+  }
+  if (a.rows > b.rows) return meet(b, a);
+  for (int64_t i = 0; i < a.rows; ++i) {  // rows j of b: -a.width < gap + i a.pitch - j b.pitch < b.width
+    const int64_t from = gap + i * a.pitch;
+    if (b.rows == 1) {
+      if (from > -a.width && from < b.width) return true;
+      continue;
+    }
+    const int64_t lo = floor_div(from - b.width, b.pitch) + 1, hi = -floor_div(-from - a.width, b.pitch) - 1;
+    if (std::max<int64_t>(lo, 0) <= std::min(hi, b.rows - 1)) return true;
+  }
+  return false;
+}
+
+void apart(const Bytes& out, const char* out_name, const Bytes& in, const char* name) {
+  if (meet(out, in)) throw Refused(std::string(out_name) + " must not overlap " + name);
+}
+
+// An output that may be this input itself, and must not overlap it otherwise.
+void same_or_apart(const Bytes& out, const char* out_name, const Bytes& in, const char* name) {
+  if (!out.same(in) && meet(out, in))
+    throw Refused(std::string(out_name) + " must be " + name + " itself, with its pitch, or not overlap it");
 }
 
 int32_t* status_of(PyObject* o, int dev) {
@@ -268,7 +321,8 @@ PyObject* rms_norm(PyObject*, PyObject* const* a, Py_ssize_t nargs) {
         h = tensor(a[6], "sum_out");
         lds = pitch(h, "sum_out", dev, rows, cols);
         typed(h, "sum_out", r.scalar_type());
-        if (x.numel() > 0 && h.data_ptr() == x.data_ptr()) throw Refused("sum_out must not be x");
+        apart(bytes_of(h, lds), "sum_out", bytes_of(x, ldx), "x");
+        same_or_apart(bytes_of(h, lds), "sum_out", bytes_of(r, ldr), "residual");
       }
     } else if (!none(a[6])) {
       throw Refused("sum_out needs a residual");
@@ -278,6 +332,7 @@ PyObject* rms_norm(PyObject*, PyObject* const* a, Py_ssize_t nargs) {
       const at::Tensor& w = tensor(a[1], "weight");
       wd = dtype_of(w, "weight");
       wp = flat(w, "weight", dev, w.scalar_type(), {cols});
+      if (!none(a[6])) apart(bytes_of(h, lds), "sum_out", bytes_of(w), "weight");
     }
     at::Tensor y, q, s;
     if (want_y) y = empty({rows, cols}, at::kBFloat16, dev);
@@ -384,6 +439,14 @@ PyObject* linear_scaled(PyObject*, PyObject* const* a, Py_ssize_t nargs) {
     }
     int32_t* status = status_of(a[6], dev);
     at::Tensor Y = output(a[5], dev, n, out, &ldy);
+    if (!none(a[5])) {
+      const Bytes y = bytes_of(Y, ldy);
+      apart(y, "out", bytes_of(X, ldx), "Xq");
+      apart(y, "out", bytes_of(W, ldw), "Wq");
+      apart(y, "out", bytes_of(THPVariable_Unpack(a[1])), "x_scale");
+      apart(y, "out", bytes_of(THPVariable_Unpack(a[3])), "w_scale");
+      if (add) same_or_apart(y, "out", bytes_of(THPVariable_Unpack(a[4]), ldadd), "add");
+    }
     launch(dev, "ar_linear_scaled", [&] {
       return ar_linear_scaled(static_cast<const uint8_t*>(X.data_ptr()), ldx, static_cast<const float*>(xs), n, in,
                               static_cast<const uint8_t*>(W.data_ptr()), ldw, static_cast<const float*>(ws), out,
@@ -420,7 +483,13 @@ PyObject* grouped_linear(PyObject*, PyObject* const* a, Py_ssize_t nargs) {
     int32_t* status = status_of(a[5], dev);
     int64_t ldy = out;
     at::Tensor Y = output(a[4], dev, n, out, &ldy);
-    if (n > 0 && Y.data_ptr() == X.data_ptr()) throw Refused("out must not be X");
+    if (!none(a[4])) {
+      const Bytes y = bytes_of(Y, ldy);
+      apart(y, "out", bytes_of(X, ldx), "X");
+      apart(y, "out", bytes_of(W, ldw), "W_hi");
+      if (lo) apart(y, "out", bytes_of(THPVariable_Unpack(a[3]), ldw), "W_lo");
+      apart(y, "out", bytes_of(THPVariable_Unpack(a[1])), "offsets");
+    }
     launch(dev, "ar_grouped_linear", [&] {
       return ar_grouped_linear(static_cast<const uint16_t*>(X.data_ptr()), ldx, n, in,
                                static_cast<const int32_t*>(offsets), experts,
@@ -450,6 +519,14 @@ PyObject* grouped_linear_scaled(PyObject*, PyObject* const* a, Py_ssize_t nargs)
     int32_t* status = status_of(a[6], dev);
     int64_t ldy = out;
     at::Tensor Y = output(a[5], dev, n, out, &ldy);
+    if (!none(a[5])) {
+      const Bytes y = bytes_of(Y, ldy);
+      apart(y, "out", bytes_of(X, ldx), "Xq");
+      apart(y, "out", bytes_of(W, ldw), "Wq");
+      apart(y, "out", bytes_of(THPVariable_Unpack(a[1])), "x_scale");
+      apart(y, "out", bytes_of(THPVariable_Unpack(a[4])), "w_scale");
+      apart(y, "out", bytes_of(THPVariable_Unpack(a[2])), "offsets");
+    }
     launch(dev, "ar_grouped_linear_scaled", [&] {
       return ar_grouped_linear_scaled(static_cast<const uint8_t*>(X.data_ptr()), ldx, static_cast<const float*>(xs), n, in,
                                       static_cast<const int32_t*>(offsets), experts,

@@ -2,6 +2,8 @@
 overlapping tensors, the memory of calls on a given stream.  Formulas in 64 bits, roundings in
 units u = 2^-24 as in test_gpu_scaled.py.
 """
+import random
+
 import pytest
 import torch
 
@@ -178,3 +180,84 @@ def test_status_word_is_kept_for_a_given_stream(ar, name):
     assert not side.query(), "the call's stream was done before the word was asked for"
     assert place not in places
     torch.cuda.synchronize()
+
+
+def refused(call):
+    try:
+        call()
+    except ValueError:
+        return True
+    return False
+
+
+def view(buf, first, rows, cols, pitch):
+    return buf[first:].as_strided((rows, cols), (pitch, 1))
+
+
+def elements(first, rows, cols, pitch):
+    return {first + r * pitch + c for r in range(rows) for c in range(cols)}
+
+
+def test_outputs_over_inputs_are_refused(ar):
+    """out beside, between or over the rows of add, sum_out of x and the residual: refused exactly where
+    an element is shared, unless it is the input itself."""
+    rng = random.Random(3)
+    buf = torch.zeros(4096, dtype=torch.bfloat16, device="cuda")
+    seen = {True: 0, False: 0}
+    for i in range(400):
+        rows, cols = rng.randint(1, 6), rng.randint(1, 12)
+        xq, xs = ar.quant_scaled(torch.ones(rows, 16, dtype=torch.bfloat16, device="cuda"))
+        wq, ws = ar.quant_scaled(torch.ones(cols, 16, dtype=torch.bfloat16, device="cuda"), 128)
+        x = torch.ones(rows, cols, dtype=torch.bfloat16, device="cuda")
+        p1 = cols + rng.choice([0, 1, 5, 13, 40])
+        p2 = rng.choice([p1, p1, cols + rng.choice([0, 1, 7, 30])])
+        o1 = rng.randint(0, 200)
+        o2 = o1 + rng.choice([0, 0, 1, cols, -cols, p1, rng.randint(-60, 60), rng.randint(-200, 200)])
+        if o2 < 0:
+            continue
+        a, b = view(buf, o1, rows, cols, p1), view(buf, o2, rows, cols, p2)
+        shared = bool(elements(o1, rows, cols, p1) & elements(o2, rows, cols, p2))
+        itself = o1 == o2 and (p1 == p2 or rows == 1)
+        seen[shared] += 1
+        assert refused(lambda: ar.linear_scaled(xq, xs, wq, ws, add=a, out=b)) == (shared and not itself)
+        assert refused(lambda: ar.rms_norm(x, None, residual=a, sum_out=b)) == (shared and not itself)
+        assert refused(lambda: ar.rms_norm(a, None, residual=x, sum_out=b)) == shared
+        weight = view(buf, o1, 1, cols, cols)[0]
+        assert refused(lambda: ar.rms_norm(x, weight, residual=x.clone(), sum_out=b)) == bool(
+            elements(o1, 1, cols, cols) & elements(o2, rows, cols, p2))
+    assert min(seen.values()) > 50
+
+
+def test_product_outputs_over_operands_are_refused(ar):
+    """out in the memory of any operand of the three products."""
+    n, inn, out = 8, 256, 128
+    raw = torch.zeros(1 << 20, dtype=torch.uint8, device="cuda")
+    Y = raw[:n * out * 2].view(torch.bfloat16).view(n, out)   # 2048 bytes
+    x = torch.ones(n, inn, dtype=torch.bfloat16, device="cuda")
+    w = torch.ones(2, out, inn, dtype=torch.bfloat16, device="cuda")
+    (xq, xs), (wq, ws) = ar.quant_scaled(x), ar.quant_scaled(w, 128)
+    offsets = torch.tensor([0, 4, n], dtype=torch.int32, device="cuda")
+
+    def placed(t, at):  # a copy of t from byte `at` of raw on
+        size = t.numel() * t.element_size()
+        raw[at:at + size].copy_(t.contiguous().view(torch.uint8).view(-1) if t.dtype.itemsize > 1 else t.view(torch.uint8).view(-1))
+        return raw[at:at + size].view(t.dtype).view(t.shape)
+
+    for at, bad in ((1024, True), (2032, True), (2048, False), (4096, False)):
+        for i in range(4):
+            o = [xq, xs, wq[0], ws[0]]
+            o[i] = placed(o[i], at)
+            assert refused(lambda: ar.linear_scaled(*o, out=Y)) == bad, (at, i)
+        for i in range(4):
+            o = [x, offsets, w, w]
+            o[i] = placed(o[i], at)
+            assert refused(lambda: ar.grouped_linear(*o, out=Y)) == bad, (at, i)
+        for i in range(5):
+            o = [xq, xs, offsets, wq, ws]
+            o[i] = placed(o[i], at)
+            assert refused(lambda: ar.grouped_linear_scaled(*o, out=Y)) == bad, (at, i)
+    # rows that overlap one another, as in an expanded tensor, are the library's to refuse
+    with pytest.raises(ar.ArError):
+        ar.linear_scaled(xq, xs, wq[0], ws[0], add=Y[:1].expand(n, out), out=Y)
+    with pytest.raises(ar.ArError):
+        ar.linear_scaled(xq, xs, wq[0], ws[0], add=torch.zeros_like(Y), out=Y[:1].expand(n, out))
