@@ -147,10 +147,12 @@ def test_outputs_on_a_given_stream_may_be_dropped_by_the_current_one(ar, name):
         got = call(side)
         places = {t.data_ptr() for t in got}
         torch.cuda.current_stream().wait_stream(side)
-        torch.cuda._sleep(20_000_000)
+        torch.cuda._sleep(100_000_000)        # (about 50 ms)
         copies = [g.view(torch.uint8) + 0 for g in got]
         del got
-        assert not places & {t.data_ptr() for t in call(side)}
+        again = {t.data_ptr() for t in call(side)}
+        assert not torch.cuda.current_stream().query(), "the outputs were read before the next call"
+        assert not places & again
         torch.cuda.synchronize()
         for c, w in zip(copies, want):
             assert torch.equal(c, w.view(torch.uint8))
