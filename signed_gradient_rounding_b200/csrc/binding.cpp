@@ -359,7 +359,8 @@ PyObject* quant_scaled(PyObject*, PyObject* const* a, Py_ssize_t nargs) {
     const int dev = device_of(x, "x");
     const ar_dtype xd = dtype_of(x, "x");
     const CallStream st(a[2], dev);
-    const int64_t block_rows = integer(a[1]);
+    // (anything else than the two becomes 0, which the library refuses: a number past 32 bits must not become one of them)
+    const int64_t asked = integer(a[1]), block_rows = asked == 1 || asked == 128 ? asked : 0;
     const bool stack = x.dim() == 3;
     const int64_t ldx = stack ? stack_pitch(x, "x") : pitch(x, "x");
     const int64_t count = stack ? x.size(0) : 1, rows = x.size(-2), cols = x.size(-1);

@@ -263,3 +263,10 @@ def test_product_outputs_over_operands_are_refused(ar):
         ar.linear_scaled(xq, xs, wq[0], ws[0], add=Y[:1].expand(n, out), out=Y)
     with pytest.raises(ar.ArError):
         ar.linear_scaled(xq, xs, wq[0], ws[0], add=torch.zeros_like(Y), out=Y[:1].expand(n, out))
+
+
+@pytest.mark.parametrize("block_rows", [0, -1, 2, 127, 129, 1 + (1 << 32), 128 + (1 << 32), 1 - (1 << 32), (1 << 63) - 1])
+def test_quant_scaled_refuses_other_blocks(ar, block_rows):
+    """Numbers that are 1 or 128 in their low 32 bits among them: the scales would have another shape."""
+    with pytest.raises(ar.ArError):
+        ar.quant_scaled(torch.ones(300, 256, dtype=torch.bfloat16, device="cuda"), block_rows)
