@@ -32,7 +32,8 @@ ar_status check_product(const void* X, int64_t ldx, int64_t n, int64_t in, const
   if (n < 0 || in <= 0 || out <= 0 || experts <= 0) return AR_EINVAL;
   if (in % (16 / el) != 0 || ldx % (16 / el) != 0 || ldw % (16 / el) != 0) return AR_EINVAL;
   if (ldx < in || ldw < in || ldy < out) return AR_EINVAL;
-  if (n > kMaxRows || in >= (1ll << 30) || experts > ar::kMaxExperts || experts * out > kMaxRows) return AR_EUNSUPPORTED;
+  if (n > kMaxRows || in >= (1ll << 30) || experts > ar::kMaxExperts || out > kMaxRows || experts * out > kMaxRows)
+    return AR_EUNSUPPORTED;
   if (ldx >= (1ll << 38) || ldw >= (1ll << 38)) return AR_EUNSUPPORTED;  // the tensor maps' pitches
   if (n == 0) return AR_OK;
   if (!X || !W || !Y || !aligned(X, 16) || !aligned(W, 16) || !aligned(Y, 2)) return AR_EINVAL;
