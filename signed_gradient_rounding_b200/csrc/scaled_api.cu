@@ -11,6 +11,8 @@
 namespace {
 
 constexpr int64_t kMaxRows = 1ll << 30;  // row indices, and their tiles' ends, in 32 bits
+// Row quantisers: the most 128-column blocks whose grid has below 2^31 CTAs of 8 warps, at two a warp (unaligned rows).
+constexpr int64_t kMaxRowBlocks = 16 * ((1ll << 31) - 1);
 
 bool aligned(const void* p, uintptr_t a) { return reinterpret_cast<uintptr_t>(p) % a == 0; }
 
@@ -96,7 +98,7 @@ ar_status ar_quant_scaled(const void* x, ar_dtype x_dtype, int64_t ldx, int64_t 
   cudaStream_t st = static_cast<cudaStream_t>(stream);
   if (block_rows == 1) {
     // rows of every matrix follow one another: one matrix of count * rows rows
-    if (count * rows * blocks_of(cols) > (1ll << 36)) return AR_EUNSUPPORTED;  // grid size
+    if (count * rows > kMaxRowBlocks / blocks_of(cols)) return AR_EUNSUPPORTED;
     if (fault_is("launch")) return AR_ECUDA;
     ar::RowQuantArgs a;
     a.x = x;
@@ -134,7 +136,7 @@ ar_status ar_silu_mul_scaled(const uint16_t* a, int64_t lda, const uint16_t* b, 
   if (rows == 0 || cols == 0) return AR_OK;
   if (!a || !b || !q || !scale || lda < cols || ldb < cols || ldq < cols) return AR_EINVAL;
   if (!aligned(a, 2) || !aligned(b, 2) || !aligned(scale, 4)) return AR_EINVAL;
-  if (rows > kMaxRows || cols > kMaxRows || rows > (1ll << 36) / blocks_of(cols)) return AR_EUNSUPPORTED;
+  if (rows > kMaxRows || cols > kMaxRows || rows > kMaxRowBlocks / blocks_of(cols)) return AR_EUNSUPPORTED;
   if (fault_is("launch")) return AR_ECUDA;
   ar::RowQuantArgs r;
   r.x = a;

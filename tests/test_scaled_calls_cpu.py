@@ -40,3 +40,11 @@ def test_sizes_whose_product_overflows_are_refused(ar, out, experts):
     assert ar.lib.ar_grouped_linear(P, 256, 4, 256, P, experts, P, None, 256, out, P, out, None, None) == EUNSUPPORTED
     assert ar.lib.ar_grouped_linear_scaled(P, 256, P, 4, 256, P, experts, P, 256, P, out, P, out, None, None) == EUNSUPPORTED
     assert ar.lib.ar_linear_scaled(P, 256, P, 4, 256, P, 256, P, out, None, 0, P, out, None, None) == EUNSUPPORTED
+
+
+def test_row_quantisers_refuse_what_no_grid_holds(ar):
+    """2^35 blocks of columns, at 16 a CTA: one CTA more than a grid has."""
+    rows = 1 << 30
+    assert ar.lib.ar_quant_scaled(P, 1, 1, 32, rows, 1, 1, P, 1, P, None) == EUNSUPPORTED
+    assert ar.lib.ar_quant_scaled(P, 1, 4096, 1, rows, 4096, 1, P, 4096, P, None) == EUNSUPPORTED
+    assert ar.lib.ar_silu_mul_scaled(P, 4095, P, 4095, rows, 4095, P, 4095, P, None) == EUNSUPPORTED
