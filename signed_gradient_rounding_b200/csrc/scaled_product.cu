@@ -21,6 +21,7 @@
 #include "ar_device.cuh"
 #include "ar_internal.h"
 #include "ar_scaled.h"
+#include "ar_units.h"
 
 namespace ar {
 
@@ -29,16 +30,8 @@ namespace {
 // Where bounded waits report when the caller passes no status word.
 __device__ int g_product_status;
 
-// Rows [r0, r1) of X that belong to expert e, clamped to the tensor: whatever the
-// offsets hold, no access leaves it.
 __device__ __forceinline__ void expert_rows(const ProductArgs& a, int e, int& r0, int& r1) {
-  if (!a.offsets) {
-    r0 = 0;
-    r1 = a.n;
-    return;
-  }
-  r0 = min(max(a.offsets[e], 0), a.n);
-  r1 = min(max(a.offsets[e + 1], r0), a.n);
+  ar::expert_rows(a.offsets, a.n, e, r0, r1);
 }
 
 // ---------------------------------------------------------------------------
@@ -52,7 +45,6 @@ constexpr int kEpiWarp0 = 4;
 constexpr int kTileThreads = 32 * kTileWarps;
 constexpr int kMaxStages = 8;
 constexpr int kRowTile = 128;     // rows per CTA: tensor-memory lanes
-constexpr int kRasterM = 8;       // row blocks that share a sweep over the weight's columns
 constexpr int kKBytes = 128;      // bytes of K per stage and row
 
 constexpr int kScaleKb = 4;     // K blocks per slot of the scale ring
@@ -101,43 +93,8 @@ struct TileCfg {
   static_assert(!kCanSplit || kStages * kStageBytes >= 128 * 128 * 4, "split-K exchange");
 };
 
-struct Unit {
-  int e;       // expert
-  int m0, r1;  // first row of X of the unit, end of the expert's rows
-  int n0;      // first column of Y
-};
-
-// Unit t in order: experts in turn; inside an expert groups of kRasterM row blocks,
-// each sweeping the weight's column blocks with the row blocks innermost (the
-// group's rows of X stay in L2 while the weight passes by).
 __device__ __forceinline__ Unit find_unit(const ProductArgs& a, const int* cum, int64_t t, int num_n, int bm, int bn) {
-  Unit u;
-  const int mb = static_cast<int>(t / num_n);
-  int e = 0;
-  if (a.offsets) {
-    int lo = 0, hi = a.experts;  // the last e with cum[e] <= mb
-    while (hi - lo > 1) {
-      const int mid = (lo + hi) >> 1;
-      if (cum[mid] <= mb)
-        lo = mid;
-      else
-        hi = mid;
-    }
-    e = lo;
-  }
-  int r0;
-  expert_rows(a, e, r0, u.r1);
-  const int64_t r = t - static_cast<int64_t>(cum[e]) * num_n;
-  const int num_m = cum[e + 1] - cum[e];
-  const int64_t per = static_cast<int64_t>(kRasterM) * num_n;
-  const int grp = static_cast<int>(r / per);
-  const int in_grp = static_cast<int>(r - grp * per);
-  const int gm = min(kRasterM, num_m - grp * kRasterM);
-  const int n_blk = in_grp / gm;
-  u.e = e;
-  u.m0 = r0 + (grp * kRasterM + in_grp - n_blk * gm) * bm;
-  u.n0 = n_blk * bn;
-  return u;
+  return ar::find_unit(a.offsets, a.n, a.experts, cum, t, num_n, bm, bn);
 }
 
 __device__ __forceinline__ uint32_t pack2(float lo, float hi) {
@@ -527,21 +484,18 @@ __global__ void __launch_bounds__(kTileThreads, 1)
   }
   chain_wait();  // (barriers and tensor memory, above, are this block's own)
   if (warp == 2) {
-    // Row blocks before each expert.  Capped at what monotone offsets can give, so
-    // that no offsets overflow the count.
+    // Row blocks before each expert.
     if (!args.offsets) {
       if (lane == 0) {
         sm->cum[0] = 0;
         sm->cum[1] = (args.n + C::kBM - 1) / C::kBM;
       }
     } else {
-      const int limit = args.n / C::kBM + args.experts;
+      const int limit = most_row_blocks(args.n, args.experts, C::kBM);
       int carry = 0;
       if (lane == 0) sm->cum[0] = 0;
       for (int e0 = 0; e0 < args.experts; e0 += 32) {
-        int r0 = 0, r1 = 0;
-        if (e0 + lane < args.experts) expert_rows(args, e0 + lane, r0, r1);
-        int v = (r1 - r0 + C::kBM - 1) / C::kBM;
+        int v = e0 + lane < args.experts ? row_blocks(args.offsets, args.n, e0 + lane, C::kBM) : 0;
 #pragma unroll
         for (int o = 1; o < 32; o <<= 1) {
           const int up = __shfl_up_sync(0xffffffffu, v, o);
