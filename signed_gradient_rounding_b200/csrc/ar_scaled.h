@@ -9,6 +9,12 @@
 
 namespace ar {
 
+// The current device (one of sm_100) and its SMs.
+struct DeviceInfo {
+  int dev = 0, sms = 0;
+};
+cudaError_t device_info(DeviceInfo* d);
+
 struct RmsNormArgs {
   const void* x = nullptr;  // [rows, cols] fp32 or bf16, row pitch ldx (elements, as every pitch here)
   int x_bf16 = 1;

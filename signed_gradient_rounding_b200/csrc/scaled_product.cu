@@ -1110,28 +1110,6 @@ __global__ void __launch_bounds__(32 * kSkinnyWarps) skinny_kernel(const __grid_
 // Launch
 // ---------------------------------------------------------------------------
 
-struct DeviceInfo {
-  int dev = 0, sms = 0;
-};
-
-cudaError_t device_info(DeviceInfo* d) {
-  static std::atomic<int> sms[64];  // 0: not yet known
-  cudaError_t e = cudaGetDevice(&d->dev);
-  if (e != cudaSuccess) return e;
-  if (d->dev < 0 || d->dev >= 64) return cudaErrorInvalidDevice;
-  d->sms = sms[d->dev].load(std::memory_order_relaxed);
-  if (d->sms == 0) {
-    int major = 0;
-    e = cudaDeviceGetAttribute(&major, cudaDevAttrComputeCapabilityMajor, d->dev);
-    if (e != cudaSuccess) return e;
-    if (major != 10) return cudaErrorNoKernelImageForDevice;
-    e = cudaDeviceGetAttribute(&d->sms, cudaDevAttrMultiProcessorCount, d->dev);
-    if (e != cudaSuccess) return e;
-    sms[d->dev].store(d->sms, std::memory_order_relaxed);
-  }
-  return cudaSuccess;
-}
-
 template <bool kF8, int kNT, int kMR, int kS>
 cudaError_t launch_skinny(const ProductArgs& a, const DeviceInfo& d, cudaStream_t st) {
   using C = SkinnyCfg<kF8, kNT, kMR, kS>;
@@ -1267,6 +1245,24 @@ cudaError_t launch_type(const ProductArgs& a, const DeviceInfo& d, cudaStream_t 
 }
 
 }  // namespace
+
+cudaError_t device_info(DeviceInfo* d) {
+  static std::atomic<int> sms[64];  // 0: not yet known
+  cudaError_t e = cudaGetDevice(&d->dev);
+  if (e != cudaSuccess) return e;
+  if (d->dev < 0 || d->dev >= 64) return cudaErrorInvalidDevice;
+  d->sms = sms[d->dev].load(std::memory_order_relaxed);
+  if (d->sms == 0) {
+    int major = 0;
+    e = cudaDeviceGetAttribute(&major, cudaDevAttrComputeCapabilityMajor, d->dev);
+    if (e != cudaSuccess) return e;
+    if (major != 10) return cudaErrorNoKernelImageForDevice;
+    e = cudaDeviceGetAttribute(&d->sms, cudaDevAttrMultiProcessorCount, d->dev);
+    if (e != cudaSuccess) return e;
+    sms[d->dev].store(d->sms, std::memory_order_relaxed);
+  }
+  return cudaSuccess;
+}
 
 cudaError_t launch_product(const ProductArgs& a, cudaStream_t st) {
   DeviceInfo d;

@@ -270,8 +270,14 @@ __device__ __forceinline__ void lane_scales(const float (&f)[8], BlockScale& b0,
 // the residual are read once and the residual may be updated in place.
 // ---------------------------------------------------------------------------
 
+// Threads of a CTA with two octs each, two CTAs an SM: the most for which the register file leaves a
+// thread 40 registers (at 800 the compiler has 32, and spills two to five times as much).
+constexpr int kTwoOctThreads = 768;
+
+// Spills: up to 48 bytes a thread at two octs and 144 at four, mostly of addresses; 1024 threads of
+// four octs, or two CTAs of two, leave no more registers.
 template <bool kXBf16, int kRes, int kOcts, bool kVec>  // kRes: 0 none, 1 fp32, 2 bf16
-__global__ void __launch_bounds__(kOcts == 2 ? 704 : 1024, kOcts == 2 ? 2 : 1) rms_norm_kernel(RmsNormArgs a) {
+__global__ void __launch_bounds__(kOcts == 2 ? kTwoOctThreads : 1024, kOcts == 2 ? 2 : 1) rms_norm_kernel(RmsNormArgs a) {
   using XT = typename OctOf<kXBf16, kVec>::type;
   using RT = typename OctOf<kRes == 2, kVec>::type;
   __shared__ float partial[32];
@@ -405,12 +411,18 @@ cudaError_t launch_norm(RmsNormArgs a, bool vec, cudaStream_t st) {
     if (octs <= 64) return launch_norm_octs<kXBf16, kRes, 2>(a, vec, grid, block, st);
     return launch_norm_octs<kXBf16, kRes, 4>(a, vec, grid, block, st);
   }
-  // A CTA per row.  Two octs a thread from 512 of them (given rows for two CTAs an SM or more) up to
-  // what two CTAs of 704 threads hold; four above.  (5000 x 11008 with a bf16 residual: 119 us with
-  // one CTA an SM, 76 with two.  A pair of CTAs per row above, to have two rows an
-  // SM there too, was no faster: 2000 x 29568 103 us for 95.)
+  // A CTA per row.  Octs a thread, with both sides timed in us (bf16 residual and e4m3 out; fp32 residual
+  // and bf16 out):
+  //   up to 4096 columns, more rows than two CTAs on every SM: two.  8000 x 4096: 41 with two, 44 with one (64, 59);
+  //     8000 x 2048: 20.3, 20.5 (34, 31).  Of fewer rows each wants its latency short: one.
+  //   up to 8192 columns: one.  8000 x 5120: 56 with one, 53 with two (73, 79); 1000 x 8192: 11.9, 12.6 (14.6, 18.2).
+  //   up to what two CTAs of two octs hold: two.  5000 x 12288: 81.5 with two, 86 with four (119, 119).
+  //   above: four.  (A pair of CTAs per row, to have two rows an SM there too, was no faster: 2000 x 29568 103 us for 95.)
+  DeviceInfo d;
+  const cudaError_t e = device_info(&d);
+  if (e != cudaSuccess) return e;
   const dim3 grid(static_cast<unsigned>(a.rows));
-  const int per = octs <= 1024 ? (octs <= 512 && a.rows > 296 ? 2 : 1) : octs <= 1408 ? 2 : 4;
+  const int per = octs <= 1024 ? (octs <= 512 && a.rows > 2 * d.sms ? 2 : 1) : octs <= 2 * kTwoOctThreads ? 2 : 4;
   const dim3 block(static_cast<unsigned>(((octs + per - 1) / per + 31) / 32 * 32));
   if (per == 1) return launch_norm_octs<kXBf16, kRes, 1>(a, vec, grid, block, st);
   if (per == 2) return launch_norm_octs<kXBf16, kRes, 2>(a, vec, grid, block, st);

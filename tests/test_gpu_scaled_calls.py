@@ -270,3 +270,24 @@ def test_quant_scaled_refuses_other_blocks(ar, block_rows):
     """Numbers that are 1 or 128 in their low 32 bits among them: the scales would have another shape."""
     with pytest.raises(ar.ArError):
         ar.quant_scaled(torch.ones(300, 256, dtype=torch.bfloat16, device="cuda"), block_rows)
+
+
+@pytest.mark.parametrize("rows", [1, 3, 297, 700])
+@pytest.mark.parametrize("cols", [1024, 1032, 4096, 4104, 8192, 8200, 12288, 12296])
+@pytest.mark.parametrize("res", [torch.bfloat16, torch.float32])
+def test_rms_norm_where_the_threads_share_of_a_row_changes(ar, rows, cols, res):
+    """Widths and row counts on both sides of each rule of the norm's launch.  Tolerances as in test_gpu_scaled.py:
+    the norm within 2^-18, its one rounding to bf16 2^-8, to e4m3 2^-4 or half the subnormal step."""
+    gen = torch.Generator(device="cuda").manual_seed(cols)
+    x = torch.randn(rows, cols, generator=gen, device="cuda").to(torch.bfloat16)
+    r = (4 * torch.randn(rows, cols, generator=gen, device="cuda")).to(res)
+    w = (1 + 0.2 * torch.randn(cols, generator=gen, device="cuda")).to(torch.bfloat16)
+    y, q, s, h = ar.rms_norm(x, w, 1e-5, residual=r, want_scaled=True)
+    h64 = x.double() + r.double()
+    v = h64 / (h64.square().mean(1, keepdim=True) + 1e-5).sqrt() * w.double()
+    assert ((y.double() - v).abs() <= v.abs() * (2.0 ** -8 + 2.0 ** -18) + 2.0 ** -133).all()
+    assert ((h.double() - h64).abs() <= h64.abs() * (2.0 ** -8 + 2 * U if res == torch.bfloat16 else U) + 2.0 ** -133).all()
+    top = torch.nn.functional.pad(v.abs(), (0, -cols % 128)).view(rows, -1, 128).amax(2) / 448
+    assert ((s.double() - top).abs() <= top * (2.0 ** -18 + 2 * U)).all()
+    u = v / top.repeat_interleave(128, 1)[:, :cols]
+    assert ((q.double() - u).abs() <= u.abs() * (2.0 ** -4 + 2.0 ** -16 + 8 * U) + 2.0 ** -10).all()
