@@ -291,3 +291,47 @@ def test_rms_norm_where_the_threads_share_of_a_row_changes(ar, rows, cols, res):
     assert ((s.double() - top).abs() <= top * (2.0 ** -18 + 2 * U)).all()
     u = v / top.repeat_interleave(128, 1)[:, :cols]
     assert ((q.double() - u).abs() <= u.abs() * (2.0 ** -4 + 2.0 ** -16 + 8 * U) + 2.0 ** -10).all()
+
+
+@pytest.mark.parametrize("name", NAMES)
+def test_given_stream_inside_a_capture(ar, name):
+    """A call on a stream that a capture has forked to, joined again: replays give the same bits, and the
+    graph's memory stays its own."""
+    call = calls_on(ar)[name]
+    want = [t.clone() for t in call(None)]
+    side = torch.cuda.Stream()
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        here = torch.cuda.current_stream()
+        side.wait_stream(here)
+        got = call(side)
+        here.wait_stream(side)
+        again = call(None)
+    noise = [call(side) for _ in range(3)]
+    for _ in range(3):
+        for t in (*got, *again):
+            t.view(torch.uint8).zero_()
+        graph.replay()
+        torch.cuda.synchronize()
+        for g, a, w in zip(got, again, want):
+            assert torch.equal(g.view(torch.uint8), w.view(torch.uint8)) and torch.equal(a.view(torch.uint8), w.view(torch.uint8))
+    torch.cuda.synchronize()
+    for ts in noise:
+        for t, w in zip(ts, want):
+            assert torch.equal(t.view(torch.uint8), w.view(torch.uint8))
+
+
+@pytest.mark.parametrize("name", NAMES)
+def test_default_and_current_stream_as_the_given_one(ar, name):
+    call = calls_on(ar)[name]
+    want = call(None)
+    for stream in (torch.cuda.default_stream(), torch.cuda.current_stream()):
+        for t, w in zip(call(stream), want):
+            assert torch.equal(t.view(torch.uint8), w.view(torch.uint8))
+    side = torch.cuda.Stream()
+    torch.cuda.synchronize()
+    with torch.cuda.stream(side):
+        got = call(torch.cuda.default_stream())
+    torch.cuda.synchronize()
+    for t, w in zip(got, want):
+        assert torch.equal(t.view(torch.uint8), w.view(torch.uint8))
