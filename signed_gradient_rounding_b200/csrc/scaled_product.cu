@@ -30,10 +30,6 @@ namespace {
 // Where bounded waits report when the caller passes no status word.
 __device__ int g_product_status;
 
-__device__ __forceinline__ void expert_rows(const ProductArgs& a, int e, int& r0, int& r1) {
-  ar::expert_rows(a.offsets, a.n, e, r0, r1);
-}
-
 // ---------------------------------------------------------------------------
 // Tile kernel
 // ---------------------------------------------------------------------------
@@ -92,10 +88,6 @@ struct TileCfg {
   static constexpr bool kCanSplit = !kPair && kBN == 128;
   static_assert(!kCanSplit || kStages * kStageBytes >= 128 * 128 * 4, "split-K exchange");
 };
-
-__device__ __forceinline__ Unit find_unit(const ProductArgs& a, const int* cum, int64_t t, int num_n, int bm, int bn) {
-  return ar::find_unit(a.offsets, a.n, a.experts, cum, t, num_n, bm, bn);
-}
 
 __device__ __forceinline__ uint32_t pack2(float lo, float hi) {
   const __nv_bfloat162 h = __floats2bfloat162_rn(lo, hi);
@@ -491,11 +483,11 @@ __global__ void __launch_bounds__(kTileThreads, 1)
         sm->cum[1] = (args.n + C::kBM - 1) / C::kBM;
       }
     } else {
-      const int limit = most_row_blocks(args.n, args.experts, C::kBM);
+      const int limit = most_row_blocks(args, C::kBM);
       int carry = 0;
       if (lane == 0) sm->cum[0] = 0;
       for (int e0 = 0; e0 < args.experts; e0 += 32) {
-        int v = e0 + lane < args.experts ? row_blocks(args.offsets, args.n, e0 + lane, C::kBM) : 0;
+        int v = e0 + lane < args.experts ? row_blocks(args, e0 + lane, C::kBM) : 0;
 #pragma unroll
         for (int o = 1; o < 32; o <<= 1) {
           const int up = __shfl_up_sync(0xffffffffu, v, o);

@@ -13,18 +13,23 @@ CSRC = os.path.join(os.path.dirname(os.path.dirname(os.path.abspath(__file__))),
 # cum as the kernel's warp scan gives it (32 experts at a time); units[t] = (e, m0, r1, n0)
 SOURCE = r"""
 #include "ar_units.h"
+struct Args {
+  int n, experts;
+  const int32_t* offsets;
+};
 extern "C" long long walk(const int32_t* offsets, int n, int experts, int num_n, int bm, int bn, int* cum, int* units,
                           long long first, long long room) {
+  const Args a = {n, experts, offsets};
   if (!offsets) {
     cum[0] = 0;
     cum[1] = (n + bm - 1) / bm;
   } else {
-    const int limit = ar::most_row_blocks(n, experts, bm);
+    const int limit = ar::most_row_blocks(a, bm);
     int carry = cum[0] = 0;
     for (int e0 = 0; e0 < experts; e0 += 32) {
       long long v = 0;
       for (int lane = 0; lane < 32; ++lane) {
-        if (e0 + lane < experts) v += ar::row_blocks(offsets, n, e0 + lane, bm);
+        if (e0 + lane < experts) v += ar::row_blocks(a, e0 + lane, bm);
         if (carry + v > 2147483647ll) return -1;
         const int c = carry + v < limit ? static_cast<int>(carry + v) : limit;
         if (e0 + lane < experts) cum[e0 + lane + 1] = c;
@@ -34,7 +39,7 @@ extern "C" long long walk(const int32_t* offsets, int n, int experts, int num_n,
   }
   const long long total = static_cast<long long>(cum[experts]) * num_n;
   for (long long t = first; t < total && t < first + room; ++t, units += 4) {
-    const ar::Unit u = ar::find_unit(offsets, n, experts, cum, t, num_n, bm, bn);
+    const ar::Unit u = ar::find_unit(a, cum, t, num_n, bm, bn);
     units[0] = u.e, units[1] = u.m0, units[2] = u.r1, units[3] = u.n0;
   }
   return total;
