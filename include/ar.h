@@ -39,6 +39,9 @@
  *       AR_FAULT=bounds  with AR_CHECKS, the step kernels are told that V and D hold
  *                        one element fewer than they do: their last store is
  *                        refused and reported (AR_ECHECK from ar_tune_status).
+ *       AR_FAULT=wait    the tile kernel of the scaled and grouped products gets no
+ *                        operands, so its bounded waits run out (after 2 ms instead
+ *                        of a second): *status AR_ETIMEOUT, Y left as it was.
  *       AR_CHECKS=1      the tuning kernels check every store to V, V_best, D, the
  *                        clip factors, the Gram matrices, the residual and the
  *                        outputs against the buffer sizes; a store outside is

@@ -123,6 +123,7 @@ struct ProductArgs {
   int split = 1;                     // CTAs of a cluster that share K (set by the launch)
   int* status = nullptr;             // null: a word of the library's
   uint64_t timeout_ns = 1000000000ull;
+  int starve = 0;                    // test hook: the tiles' producers bring nothing, so every wait behind them runs out
 };
 constexpr int kMaxExperts = 1024;
 

@@ -27,6 +27,13 @@ bool dtype_ok(ar_dtype t) { return t == AR_F32 || t == AR_BF16; }
 
 ar_status from_cuda(cudaError_t e) { return e == cudaSuccess ? AR_OK : AR_ECUDA; }
 
+// AR_FAULT=wait: the tile kernel's waits run out, after 2 ms.
+void wait_hook(ar::ProductArgs& a) {
+  if (!fault_is("wait")) return;
+  a.starve = 1;
+  a.timeout_ns = 2000000;
+}
+
 // The checks that the three products share.  el: bytes per operand element.
 ar_status check_product(const void* X, int64_t ldx, int64_t n, int64_t in, const void* W, int64_t ldw, int64_t experts,
                         int64_t out, const void* Y, int64_t ldy, int el) {
@@ -180,6 +187,7 @@ ar_status ar_linear_scaled(const uint8_t* X, int64_t ldx, const float* x_scale, 
   a.ldy = ldy;
   a.vec_y = aligned(Y, 16) && ldy % 8 == 0 && (!add || (aligned(add, 16) && ldadd % 8 == 0));
   a.status = status;
+  wait_hook(a);
   return from_cuda(ar::launch_product(a, static_cast<cudaStream_t>(stream)));
 }
 
@@ -207,6 +215,7 @@ ar_status ar_grouped_linear(const uint16_t* X, int64_t ldx, int64_t n, int64_t i
   a.ldy = ldy;
   a.vec_y = aligned(Y, 16) && ldy % 8 == 0;
   a.status = status;
+  wait_hook(a);
   return from_cuda(ar::launch_product(a, static_cast<cudaStream_t>(stream)));
 }
 
@@ -238,6 +247,7 @@ ar_status ar_grouped_linear_scaled(const uint8_t* X, int64_t ldx, const float* x
   a.ldy = ldy;
   a.vec_y = aligned(Y, 16) && ldy % 8 == 0;
   a.status = status;
+  wait_hook(a);
   return from_cuda(ar::launch_product(a, static_cast<cudaStream_t>(stream)));
 }
 

@@ -526,7 +526,7 @@ __global__ void __launch_bounds__(kTileThreads, 1)
       int stage = 0;
       uint32_t phase = 0, issued_mask = 0, issued_parity = 0;
       bool ok = true;
-      for (int64_t t = unit0; ok && t < num_units; t += stride) {
+      for (int64_t t = unit0; ok && t < num_units && !args.starve; t += stride) {
         const Unit u = find_unit(args, sm->cum, t, num_n, C::kBM, kBN);
         const int x_row = u.m0 + static_cast<int>(rank) * kRowTile;
         const int w_row = u.e * args.out + u.n0 + static_cast<int>(rank) * (C::kBRows / C::kWBoxes);
@@ -777,7 +777,10 @@ __global__ void __launch_bounds__(kTileThreads, 1)
       } else {
         RowsOut<kNC, kWhole> rows_out;
         if (!split) rows_out.begin(args, out_buf, row0, u.r1, col0, kNC, lane);
-        if (!wait_bar(my_tfull + 8 * C::kHalves * acc_buf, acc_phase, abort_flag, status, args.timeout_ns)) break;
+        if (!wait_bar(my_tfull + 8 * C::kHalves * acc_buf, acc_phase, abort_flag, status, args.timeout_ns)) {
+          ok = false;  // (a share of K that is not there is not added up)
+          break;
+        }
         tc_fence_after();
         if (!split) rows_out.ready(args, kNC);
 #pragma unroll 1

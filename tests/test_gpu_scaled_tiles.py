@@ -465,3 +465,47 @@ def test_from_tuned_layers(ar, n):  # noqa: F811
         step = exact[e].abs() * 2.0 ** -4 + ws[e].double().repeat_interleave(128, 0)[:out].repeat_interleave(128, 1)[:, :inn] * 2.0 ** -10
         assert ((w - exact[e]).abs() <= step * (1 + 2.0 ** -18)).all()
         at += c
+
+
+@pytest.mark.parametrize("kind", ["scaled", "bf16"])
+@pytest.mark.parametrize("form", list(GROUPED))
+def test_waits_that_run_out_end_the_call(ar, form, kind, tmp_path, monkeypatch):  # noqa: F811
+    """No operands ever come: every role gives up, the status word says so, nothing is written, and the calls
+    behind it in the stream and after it are as ever."""
+    pair, bn, counts, inn, out = GROUPED[form]
+    p = Experts(ar, kind, counts, inn, out, 7)
+    want = torch.full((p.n, out), 3.0, dtype=torch.bfloat16, device="cuda")
+    check_tile(lambda: p(want), kind, pair, bn, True, tmp_path)
+    want.fill_(3.0)
+    p(want)
+    buf = torch.full((p.n + 200, out), 3.0, dtype=torch.bfloat16, device="cuda")
+    Y, after = buf[100:100 + p.n], torch.full_like(want, 3.0)
+    status, clean = (torch.zeros(1, dtype=torch.int32, device="cuda") for _ in range(2))
+    torch.cuda.synchronize()
+    begin, end = (torch.cuda.Event(enable_timing=True) for _ in range(2))
+    begin.record()
+    monkeypatch.setenv("AR_FAULT", "wait")
+    p(Y, status=status)
+    p(Y)  # without a word
+    monkeypatch.delenv("AR_FAULT")
+    end.record()
+    p(after, status=clean)
+    torch.cuda.synchronize()
+    assert status.item() == ar.AR_ETIMEOUT and (buf == 3).all() and 4 <= begin.elapsed_time(end) < 500
+    assert clean.item() == 0 and torch.equal(after, want)
+
+
+@pytest.mark.parametrize("form", list(DENSE))
+def test_waits_that_run_out_leave_the_residual(ar, form, monkeypatch):  # noqa: F811
+    """The dense product with its residual in place, aligned and not."""
+    pair, bn, n, inn, out = DENSE[form]
+    for odd in (0, 3):
+        ops = scaled_operands(ar, n, inn, out - odd, 5)
+        add = rand(6, n, out - odd)
+        stream, status = add.clone(), torch.zeros(1, dtype=torch.int32, device="cuda")
+        monkeypatch.setenv("AR_FAULT", "wait")
+        ar.linear_scaled(*ops, add=stream, out=stream, status=status)
+        monkeypatch.delenv("AR_FAULT")
+        assert status.item() == ar.AR_ETIMEOUT and torch.equal(stream, add)
+        ar.linear_scaled(*ops, add=stream, out=stream)
+        assert torch.equal(stream, ar.linear_scaled(*ops, add=add))
