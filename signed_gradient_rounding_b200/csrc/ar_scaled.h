@@ -122,7 +122,7 @@ struct ProductArgs {
   int vec_y = 0;                     // Y and add take 16-byte accesses at multiples of 8 columns
   int split = 1;                     // CTAs of a cluster that share K (set by the launch)
   int* status = nullptr;             // null: a word of the library's
-  uint64_t timeout_ns = 1000000000ull;
+  uint64_t timeout_ns = 1000000000ull;  // of one wait; the launch adds to it for K
   int starve = 0;                    // test hook: the tiles' producers bring nothing, so every wait behind them runs out
 };
 constexpr int kMaxExperts = 1024;

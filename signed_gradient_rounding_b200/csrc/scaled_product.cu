@@ -1165,6 +1165,9 @@ cudaError_t launch_tile_as(ProductArgs a, const DeviceInfo& d, cudaStream_t st, 
   const int64_t most = units_at_most(a, C::kBM, kBN);
   while (split > a.nkb) split /= 2;  // 1, 2 or 4
   a.split = split;
+  // A bf16 accumulator is handed over after all of K, so the waits' limit grows with it: 1 us a K block, of which
+  // 17 rows take 55 ns and 300 rows x 1000 columns 210.  (2^25 blocks, the longest, take 1.8 s.)
+  a.timeout_ns += 1000ull * (a.W_lo ? 2 : 1) * static_cast<uint64_t>(a.nkb);
   if (most < units || split > 1) units = static_cast<int>(most);
   CUtensorMap mx, mw, mlo;
   const uint64_t bytes = static_cast<uint64_t>(a.in) * (kF8 ? 1 : 2);

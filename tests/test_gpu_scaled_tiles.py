@@ -509,3 +509,30 @@ def test_waits_that_run_out_leave_the_residual(ar, form, monkeypatch):  # noqa: 
         assert status.item() == ar.AR_ETIMEOUT and torch.equal(stream, add)
         ar.linear_scaled(*ops, add=stream, out=stream)
         assert torch.equal(stream, ar.linear_scaled(*ops, add=add))
+
+
+def test_sums_longer_than_a_second(ar, tmp_path):  # noqa: F811
+    """So many columns that one accumulator takes more than a second: the waits for it do not run out.
+    Rows of +1, -1, ... whose last elements leave small whole numbers: every partial sum is exact."""
+    n, inn = 17, 6 << 27
+    torch.cuda.empty_cache()
+    X = torch.ones(n, inn, dtype=torch.bfloat16, device="cuda")
+    X *= torch.arange(1, n + 1, device="cuda", dtype=torch.bfloat16)[:, None]
+    hi, lo = (torch.ones(1, 1, inn, dtype=torch.bfloat16, device="cuda") for _ in range(2))
+    for w, last in ((hi, 3.0), (lo, 9.0)):
+        w[..., 1::2] = -1.0
+        w[..., -1] = last
+    status = torch.zeros(1, dtype=torch.int32, device="cuda")
+    offsets = offsets_of([n])
+    small = slice(0, 1 << 20)
+    check_tile(lambda: ar.grouped_linear(X[:, small], offsets, hi[..., small], lo[..., small]), "bf16", False, 128, False, tmp_path)
+    begin, end = (torch.cuda.Event(enable_timing=True) for _ in range(2))
+    begin.record()
+    Y = ar.grouped_linear(X, offsets, hi, lo, status=status)
+    end.record()
+    torch.cuda.synchronize()
+    del X, hi, lo
+    torch.cuda.empty_cache()
+    want = torch.arange(1, n + 1, device="cuda")[:, None] * (1.0 + 3.0 + 1.0 + 9.0)  # (at most 238: exact in bf16)
+    assert status.item() == 0 and torch.equal(Y.float(), want)
+    assert begin.elapsed_time(end) > 1000
