@@ -452,8 +452,9 @@ ar_status ar_silu_mul_scaled(const uint16_t* a, int64_t lda, const uint16_t* b, 
 
 /* Y = bf16(X W^T + add) of scaled tensors, on the tensor cores:
  *     Y[n, o] = sum_b x_scale[n, b] * w_scale[o/128, b] * sum_{k in block b} X[n, k] * W[o, k]
- * each block's products summed by the tensor cores in fp32, the blocks added in fp32 in
- * order within a share of K and the shares in order, one rounding to bf16.
+ * each block's products summed by the tensor cores in fp32, x_scale * w_scale formed first
+ * (in fp32: the two together must stay in its range), the blocks added in fp32 in order
+ * within a share of K and the shares in order, one rounding to bf16.
  *   X [n, in], W [out, in]: e4m3, 16-byte aligned, `in` and the pitches multiples of 16.
  *   add [n, out] bf16 or NULL, added in fp32;  Y [n, out] bf16 out (must not overlap an
  *   input, unless it is add itself with the same pitch).

@@ -516,7 +516,8 @@ __global__ void __launch_bounds__(kTileThreads, 1)
   const uint32_t bar_full = smem_u32(sm->full), bar_empty = smem_u32(sm->empty);
   const uint32_t bar_tfull = smem_u32(sm->tfull), bar_tempty = smem_u32(sm->tempty);
 
-  // Registers: the launch's 12 warps at 168 become 4 at 56 and 8 at 224.
+  // Registers: the launch's 12 warps at 168 become 4 at 56 and 8 at 224.  The compiler allots 168 to all: the
+  // e4m3 forms (128 sums, 64 columns in flight) spill 44 to 104 bytes a thread there, the bf16 ones none.
   if (warp < kEpiWarp0) {
     asm volatile("setmaxnreg.dec.sync.aligned.u32 56;");
     if (warp == 0) {
@@ -1199,6 +1200,8 @@ cudaError_t launch_tile(const ProductArgs& a, const DeviceInfo& d, cudaStream_t 
 // Several experts are taken to be uneven (some have several times the average):
 //   64 experts, 4096 -> 2048, 4 rows each: 83 and 115; 8: 102 and 107; 12: 117 and 108
 //   the same in bf16, 8 rows each: 187 and 183; 12: 220 and 184
+// Only the average is known here: an expert with many more rows walks its W once per 8 or 16 of them, alone.
+//   256 experts, 2048 -> 1024, 1024 rows: 108 drawn evenly (10 rows at most), 178 with 411 in one expert.
 // Of the skinny kernel's shapes, two strips of W per CTA and two blocks per warp in flight won
 // over one strip (51 and 69 for 64 experts with 64 rows) and over more blocks (three: 70;
 // shared memory then holds fewer CTAs); 8 rows of X per pass while there are no more, 16 up to 16.

@@ -447,7 +447,7 @@ constexpr int kUnitsOf = kVec ? 4 : 1;
 // those).  f / 128 is exact for every bf16.  Relative error below 2^-20 + |f| 2^-23: the argument
 // f log2(e) - 7 is rounded once, ex2 and rcp are within 2 units.  With the library's expf and
 // division the kernel was bound by its instructions: 33 per element, 217 us for 16384 x 11008
-// where the memory takes 139.  exp(-f) = inf gives f * 0 = -0, the limit.
+// where the memory takes 139; so it takes 182 (180 with the plain sum).  exp(-f) = inf gives f * 0 = -0, the limit.
 __device__ __forceinline__ float silu(float f) {
   float e, r;
   asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(e) : "f"(__fmaf_rn(f, -1.44269504088896341f, -7.0f)));
@@ -537,6 +537,7 @@ __global__ void __launch_bounds__(256, kVec ? 4 : 1) row_quant_kernel(RowQuantAr
 // ---------------------------------------------------------------------------
 // Weight quantiser: a CTA per 128 x 128 tile.  Thread t owns the oct t % 16 of the
 // rows t / 16 + 32 i, i < 4, in registers between the tile's maximum and the store.
+// (fp32 input, and unaligned rows; two CTAs an SM leave 64 registers, of which 24 to 104 bytes spill.)
 // ---------------------------------------------------------------------------
 
 template <bool kXBf16, bool kVec>
