@@ -18,7 +18,7 @@ from tests.test_gpu_scaled import (ar, check_product, layer, layer_weights, nblk
 pytestmark = pytest.mark.gpu
 
 
-def launched(call, path="/tmp"):
+def launched(call, path):
     """The kernels that `call` launches, as (name, template arguments, CTAs), from a graph that captures it."""
     call()  # (not the first call in a capture: that has a test of its own)
     graph = torch.cuda.CUDAGraph(keep_graph=True)
